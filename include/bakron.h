@@ -367,6 +367,95 @@ bakron_status_t bakron_proxy_loss(const float *W_dev, const float *V_dev, const 
                                   double *out_host, void *ws_dev, size_t ws_bytes,
                                   bakron_stream_t stream);
 
+/* ------------------------------------- products over packed rows, 8 bits */
+/* No counterpart in the paper: what a program does with quantised weight
+ * matrices, and what a layer of several expert matrices needs before them.
+ *
+ * Packed rows: the rows of all groups (the tokens of each expert) one after
+ * another in one matrix; offsets_dev holds experts + 1 int32 row bounds on the
+ * device, group e being rows offsets[e] .. offsets[e+1] - 1.  Bounds must not
+ * decrease and must lie in [0, rows]; a group may be empty.  Rows outside every
+ * group are neither read into a result nor written.  The host never reads the
+ * offsets, so a call can be captured into a CUDA graph and replayed with other
+ * ones.  A group whose bounds are not a valid range counts as empty, and
+ * BAKRON_ERR_INVALID_ARG is recorded (device error).
+ *
+ * experts is 1 .. 1024, extents are at most 2^30.  Matrices are row-major with
+ * unit column stride; *_row_stride is in elements.  Operands that the tensor
+ * cores read need rows that start on 16-byte boundaries (BAKRON_ERR_ALIGNMENT):
+ * an odd width is kept in a wider row.  Results may have any row stride.
+ * All results are written in one pass in a fixed order of operations: equal
+ * calls give equal bits.  Results must not overlap the operands.
+ * Workspace: BAKRON_STATUS_BYTES (the status block) unless stated.
+ * Device errors, all of them: BAKRON_ERR_DEVICE_TIMEOUT. */
+#define BAKRON_STATUS_BYTES ((size_t)256)
+typedef enum { BAKRON_F32 = 0, BAKRON_BF16 = 1, BAKRON_F16 = 2 } bakron_type_t;
+
+/* 8-bit floating point (e4m3) codes with one fp32 step per block:
+ *   s_b = fp32(max |x_b| / 448), 1 where that is zero;
+ *   q   = the e4m3 value nearest to clamp(fp32(x / s_b), -448, 448), ties to even.
+ * x_dev: batch matrices of rows x cols (fp32, bf16 or fp16; any row stride),
+ * x_batch_stride elements apart.  block_rows 1: a step per row and 128 columns
+ * (scales batch x rows x ceil(cols/128)); 128: a step per 128 x 128 tile
+ * (scales batch x ceil(rows/128) x ceil(cols/128)); the last blocks may be
+ * ragged.  q_dev: batch x rows rows of cols codes, q_row_stride (a multiple of
+ * 16) bytes apart; bytes between cols and q_row_stride are left as they are.
+ * rows and batch may be 0.  Device errors: BAKRON_ERR_NONFINITE (x; the codes of
+ * a block that holds such a value are unspecified). */
+bakron_status_t bakron_quantize_blocks(const void *x_dev, int32_t x_type, int64_t batch, int64_t rows, int64_t cols,
+                                       int64_t x_batch_stride, int64_t x_row_stride, int32_t block_rows,
+                                       uint8_t *q_dev, int64_t q_row_stride, float *scales_dev, void *ws_dev,
+                                       size_t ws_bytes, bakron_stream_t stream);
+
+/* Product of two such operands:
+ *   y[t, i] = sum_b xs[t, b] ws(i, b) sum_{k in block b} x[t, k] w_e[i, k]
+ * x: rows x k codes, xs rows x ceil(k/128).  w: experts matrices of n x k codes,
+ * w_expert_stride (>= n * w_row_stride) bytes apart; w_scale_rows 128: steps
+ * experts x ceil(n/128) x ceil(k/128); 1: one step per row, experts x n -- the
+ * solver's steps, whose codes of up to 5 bits are e4m3 values as they stand.
+ * offsets_dev NULL with experts 1: one matrix for all rows.  y: rows x n (fp32,
+ * bf16 or fp16), rounded once from FP32 sums.  rows may be 0. */
+bakron_status_t bakron_matmul_blocks(const uint8_t *x_dev, int64_t x_row_stride, const float *x_scales_dev,
+                                     const uint8_t *w_dev, int64_t w_row_stride, int64_t w_expert_stride,
+                                     const float *w_scales_dev, int32_t w_scale_rows, const int32_t *offsets_dev,
+                                     int64_t experts, void *y_dev, int32_t y_type, int64_t y_row_stride, int64_t rows,
+                                     int64_t n, int64_t k, void *ws_dev, size_t ws_bytes, bakron_stream_t stream);
+
+/* Products grouped by expert, type (of x, dy and w) bf16 or fp16, FP32 sums,
+ * results of that type or fp32 (rounded once); w: experts matrices of n x k,
+ * w_expert_stride (>= n * w_row_stride) elements apart:
+ *   y[t, :]  = x[t, :] w_e^T       (rows x n)   for t in group e
+ *   dx[t, :] = dy[t, :] w_e        (rows x k)
+ *   dw_e     = sum_{t in group e} dy[t, :]^T x[t, :]   (experts x n x k, dense;
+ *              zeros for an empty group)
+ * the last two being the gradients of the first.  rows may be 0. */
+bakron_status_t bakron_matmul_grouped(const void *x_dev, int32_t type, int64_t x_row_stride, const void *w_dev,
+                                      int64_t w_row_stride, int64_t w_expert_stride, const int32_t *offsets_dev,
+                                      int64_t experts, void *y_dev, int32_t y_type, int64_t y_row_stride, int64_t rows,
+                                      int64_t n, int64_t k, void *ws_dev, size_t ws_bytes, bakron_stream_t stream);
+bakron_status_t bakron_matmul_grouped_dx(const void *dy_dev, int32_t type, int64_t dy_row_stride, const void *w_dev,
+                                         int64_t w_row_stride, int64_t w_expert_stride, const int32_t *offsets_dev,
+                                         int64_t experts, void *dx_dev, int32_t dx_type, int64_t dx_row_stride,
+                                         int64_t rows, int64_t n, int64_t k, void *ws_dev, size_t ws_bytes,
+                                         bakron_stream_t stream);
+bakron_status_t bakron_matmul_grouped_dw(const void *dy_dev, int32_t type, int64_t dy_row_stride, const void *x_dev,
+                                         int64_t x_row_stride, const int32_t *offsets_dev, int64_t experts,
+                                         void *dw_dev, int32_t dw_type, int64_t rows, int64_t n, int64_t k,
+                                         void *ws_dev, size_t ws_bytes, bakron_stream_t stream);
+
+/* One damped Gram factor per group of packed samples, bakron_gram for the
+ * experts of a layer:
+ *   A_e = X_e^T X_e / N_e + damping * mean_i (X_e^T X_e / N_e)_ii * I
+ * X: rows x d (fp32 with any row stride, bf16 or fp16), N_e the rows of group
+ * e; A: experts x d x d, fp32, dense, symmetric to the bit; zeros for an empty
+ * group.  fp32 samples enter as three bf16 parts (24 bits).  Device errors:
+ * BAKRON_ERR_NONFINITE (X, or a sum of squares that overflows).  Workspace:
+ * bakron_gram_grouped_workspace_size(type, rows, d) bytes. */
+size_t bakron_gram_grouped_workspace_size(int32_t type, int64_t rows, int64_t d);
+bakron_status_t bakron_gram_grouped(const void *X_dev, int32_t type, int64_t x_row_stride, const int32_t *offsets_dev,
+                                    int64_t experts, float damping, float *A_dev, int64_t rows, int64_t d,
+                                    void *ws_dev, size_t ws_bytes, bakron_stream_t stream);
+
 /* ---------------------------------------------------------- diagnostics */
 /* Synchronises `stream` and returns the first device-detected error of the
  * latest call on this workspace (BAKRON_OK if none), then clears it. */

@@ -20,7 +20,8 @@ from ._native import BakronError, BatchItem, Config, PlanStats, Profile, Profile
 
 __all__ = ["factor", "solve", "solve_host", "proxy_loss", "plan_stats", "last_profile",
            "last_profile_launches", "tune_leaf", "tune_cache_key", "tune_cache_get", "tune_cache_put",
-           "solve_batch", "gram", "selftest_wait_timeout", "selftest_band_abort", "workspace", "get_status",
+           "solve_batch", "gram", "gram_grouped", "quantize_blocks", "matmul_blocks", "matmul_grouped",
+           "matmul_grouped_dx", "matmul_grouped_dw", "selftest_wait_timeout", "selftest_band_abort", "workspace", "get_status",
            "BakronError", "Status", "version", "library_path"]
 
 
@@ -321,6 +322,235 @@ def gram(X, damping=0.0, *, ws=None, out=None, stream=None, check_status=True):
     check(lib.bakron_gram(_ptr(X), N, d, float(damping), _ptr(A), _ptr(ws), ws.numel(), st), "bakron_gram")
     if check_status:
         check(lib.bakron_get_status(_ptr(ws), ws.numel(), st), "bakron_gram (device)")
+    return A
+
+
+# ------------------------------------------------- products over packed rows
+STATUS_BYTES = 256  # workspace of the calls below that need no more than the status block
+
+_type_ids = None
+
+
+def _types():
+    """torch dtype -> bakron_type_t."""
+    global _type_ids
+    if _type_ids is None:
+        torch = _torch()
+        _type_ids = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    return _type_ids
+
+
+def _here(t, name, dims, dtypes):
+    """A CUDA tensor on the current device with unit stride along its last dimension."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes or t.dim() not in dims:
+        raise TypeError(f"{name} must be a CUDA tensor of {' or '.join(map(str, dims))} dimensions and type "
+                        f"{', '.join(str(d) for d in dtypes)}")
+    if t.device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    return t
+
+
+def _ld(t, dim, least, align):
+    """Row (or matrix) stride of a dimension; any will do where it has one entry."""
+    return t.stride(dim) if t.shape[dim] > 1 else -(-least // align) * align
+
+
+def _groups(offsets, experts=None):
+    torch = _torch()
+    _here(offsets, "offsets", (1,), (torch.int32,))
+    if offsets.shape[0] < 2 or (experts is not None and offsets.shape[0] != experts + 1):
+        raise ValueError("offsets must hold one bound more than there are experts")
+    if not offsets.is_contiguous():
+        raise ValueError("offsets must be contiguous")
+    return offsets.shape[0] - 1
+
+
+def _result(out, shape, dtype, allowed, device):
+    """The result tensor: ``out``, or a new one of ``dtype``."""
+    torch = _torch()
+    if out is None:
+        if dtype not in allowed:
+            raise TypeError(f"out_dtype must be one of {', '.join(str(d) for d in allowed)}")
+        return torch.empty(shape, dtype=dtype, device=device)
+    _here(out, "out", (len(shape),), allowed)
+    if tuple(out.shape) != tuple(shape) or (dtype is not None and out.dtype != dtype):
+        raise ValueError(f"out must have shape {tuple(shape)}" + (f" and type {dtype}" if dtype is not None else ""))
+    return out
+
+
+def _call(name, args, ws, stream, check_status, device, need=STATUS_BYTES):
+    """One library call on a workspace: ``ws``, or a new one."""
+    torch = _torch()
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _here(ws, "ws", (1,), (torch.uint8,))
+    st = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    status = getattr(_lib(), name)(*args, ws.data_ptr(), ws.numel(), st)
+    if status:
+        check(status, name)
+    if check_status:
+        check(_lib().bakron_get_status(ws.data_ptr(), ws.numel(), st), name + " (device)")
+
+
+def quantize_blocks(x, block_rows=1, *, out=None, ws=None, stream=None, check_status=True):
+    """8-bit floating point codes of ``x`` (rows x cols, or batch x rows x cols;
+    float32, bfloat16 or float16) with one float32 step per block of
+    ``block_rows`` x 128 values, ``block_rows`` 1 or 128
+    (``bakron_quantize_blocks``): ``x ~= codes * step``.
+
+    Returns ``(codes, scales)``: ``codes`` float8_e4m3fn of x's shape, with rows
+    that start on 16-byte boundaries as :func:`matmul_blocks` wants them (a view
+    of a wider buffer for odd widths), ``scales`` of shape ``[..., ceil(rows /
+    block_rows), ceil(cols / 128)]``.  ``out`` may supply both."""
+    torch = _torch()
+    _here(x, "x", (2, 3), tuple(_types()))
+    rows, cols = x.shape[-2:]
+    batch = x.shape[0] if x.dim() == 3 else 1
+    lead = tuple(x.shape[:-2])
+    steps = lead + (-(-rows // block_rows) if block_rows in (1, 128) else rows, -(-cols // 128))
+    if out is None:
+        wide = -(-cols // 16) * 16
+        q = torch.empty(lead + (rows, wide), dtype=torch.float8_e4m3fn, device=x.device)
+        q = q[..., :cols] if wide != cols else q
+        scales = torch.empty(steps, dtype=torch.float32, device=x.device)
+    else:
+        q, scales = out
+        _here(q, "codes", (x.dim(),), (torch.float8_e4m3fn,))
+        _here(scales, "scales", (x.dim(),), (torch.float32,))
+        if q.shape != x.shape or tuple(scales.shape) != steps or not scales.is_contiguous():
+            raise ValueError(f"codes must have shape {tuple(x.shape)}, scales {steps} (contiguous)")
+    ldq = _ld(q, -2, cols, 16)
+    if x.dim() == 3 and batch > 1 and rows and q.stride(0) != rows * ldq:
+        raise ValueError("codes must hold its matrices one directly after another")
+    ldx = _ld(x, -2, cols, 1)
+    _call("bakron_quantize_blocks",
+          (x.data_ptr(), _types()[x.dtype], batch, rows, cols, x.stride(0) if batch > 1 else 0, ldx, block_rows,
+           q.data_ptr(), ldq, scales.data_ptr()), ws, stream, check_status, x.device)
+    return q, scales
+
+
+def matmul_blocks(x, x_scales, w, w_scales, offsets=None, *, out_dtype=None, out=None, ws=None, stream=None,
+                  check_status=True):
+    """``y = (x * steps) (w * steps)^T`` of 8-bit (float8_e4m3fn) operands
+    (``bakron_matmul_blocks``), accumulated in float32.
+
+    ``x`` rows x k with ``x_scales`` rows x ceil(k/128), as
+    :func:`quantize_blocks` gives them; ``w`` n x k with ``w_scales`` either
+    ceil(n/128) x ceil(k/128), or of shape (n,): one step per row, as
+    :func:`solve` returns them (its codes of up to 5 bits are e4m3 values:
+    ``codes.float().to(torch.float8_e4m3fn)``).  With ``offsets`` (int32,
+    experts + 1 row bounds on the device) ``w`` is experts x n x k, the steps
+    have the same leading dimension, and rows ``offsets[e] .. offsets[e+1] - 1``
+    are multiplied by ``w[e]``; rows outside every group keep what ``out`` holds
+    (unspecified in a new result).  Result: rows x n, bfloat16 unless
+    ``out_dtype`` or ``out`` says float16 or float32."""
+    torch = _torch()
+    f8, f32 = (torch.float8_e4m3fn,), (torch.float32,)
+    _here(x, "x", (2,), f8), _here(x_scales, "x_scales", (2,), f32)
+    lead = () if offsets is None else (1,)
+    _here(w, "w", (2 + len(lead),), f8)
+    _here(w_scales, "w_scales", (1 + len(lead), 2 + len(lead)), f32)
+    rows, k = x.shape
+    n = w.shape[-2]
+    experts = 1 if offsets is None else _groups(offsets, w.shape[0])
+    per_row = w_scales.dim() == 1 + len(lead)
+    steps = tuple(w.shape[:-2]) + ((n,) if per_row else (-(-n // 128), -(-k // 128)))
+    if w.shape[-1] != k or tuple(x_scales.shape) != (rows, -(-k // 128)) or tuple(w_scales.shape) != steps:
+        raise ValueError("x is rows x k with steps rows x ceil(k/128); w is n x k with steps ceil(n/128) x "
+                         "ceil(k/128) or (n,), under one leading dimension when offsets are given")
+    if not x_scales.is_contiguous() or not w_scales.is_contiguous():
+        raise ValueError("x_scales and w_scales must be contiguous")
+    if out is None and out_dtype is None:
+        out_dtype = torch.bfloat16
+    y = _result(out, (rows, n), out_dtype, _types(), x.device)
+    ldw = _ld(w, -2, k, 16)
+    _call("bakron_matmul_blocks",
+          (x.data_ptr(), _ld(x, 0, k, 16), x_scales.data_ptr(), w.data_ptr(), ldw,
+           w.stride(0) if experts > 1 else -(-n * ldw // 16) * 16, w_scales.data_ptr(), 1 if per_row else 128,
+           offsets.data_ptr() if offsets is not None else 0, experts, y.data_ptr(), _types()[y.dtype],
+           _ld(y, 0, n, 1), rows, n, k), ws, stream, check_status, x.device)
+    return y
+
+
+def _grouped(name, x, w, offsets, across, out_dtype, out, ws, stream, check_status):
+    torch = _torch()
+    _here(x, "x" if across == 2 else "dy", (2,), (torch.bfloat16, torch.float16))
+    _here(w, "w", (3,), (x.dtype,))
+    experts = _groups(offsets, w.shape[0])
+    n, k = w.shape[1:]
+    rows = x.shape[0]
+    if x.shape[1] != w.shape[across]:
+        raise ValueError(f"{'x' if across == 2 else 'dy'} must have {w.shape[across]} columns")
+    width = w.shape[3 - across]
+    if out is None and out_dtype is None:
+        out_dtype = x.dtype
+    y = _result(out, (rows, width), out_dtype, (x.dtype, torch.float32), x.device)
+    ldw = _ld(w, 1, k, 8)
+    _call(name, (x.data_ptr(), _types()[x.dtype], _ld(x, 0, x.shape[1], 8), w.data_ptr(), ldw,
+                 w.stride(0) if experts > 1 else n * ldw, offsets.data_ptr(), experts, y.data_ptr(),
+                 _types()[y.dtype], _ld(y, 0, width, 1), rows, n, k), ws, stream, check_status, x.device)
+    return y
+
+
+def matmul_grouped(x, w, offsets, *, out_dtype=None, out=None, ws=None, stream=None, check_status=True):
+    """``y[t] = x[t] w[e]^T`` for the packed rows ``t`` of every expert e
+    (``bakron_matmul_grouped``): ``x`` rows x k, ``w`` experts x n x k, both
+    bfloat16 or float16, ``offsets`` int32 with experts + 1 row bounds on the
+    device.  Sums in float32; ``y`` rows x n of x's type or float32.  Rows
+    outside every group keep what ``out`` holds (unspecified in a new result)."""
+    return _grouped("bakron_matmul_grouped", x, w, offsets, 2, out_dtype, out, ws, stream, check_status)
+
+
+def matmul_grouped_dx(dy, w, offsets, *, out_dtype=None, out=None, ws=None, stream=None, check_status=True):
+    """Gradient of :func:`matmul_grouped` for its rows: ``dx[t] = dy[t] w[e]``
+    (``bakron_matmul_grouped_dx``)."""
+    return _grouped("bakron_matmul_grouped_dx", dy, w, offsets, 1, out_dtype, out, ws, stream, check_status)
+
+
+def matmul_grouped_dw(dy, x, offsets, *, out_dtype=None, out=None, ws=None, stream=None, check_status=True):
+    """Gradient of :func:`matmul_grouped` for its weights: ``dw[e] = sum_t
+    dy[t]^T x[t]`` over expert e's rows, experts x n x k, zeros for an expert
+    without rows (``bakron_matmul_grouped_dw``)."""
+    torch = _torch()
+    _here(dy, "dy", (2,), (torch.bfloat16, torch.float16))
+    _here(x, "x", (2,), (dy.dtype,))
+    experts = _groups(offsets)
+    rows, n = dy.shape
+    if x.shape[0] != rows:
+        raise ValueError("dy and x must have the same rows")
+    k = x.shape[1]
+    if out is None and out_dtype is None:
+        out_dtype = x.dtype
+    dw = _result(out, (experts, n, k), out_dtype, (x.dtype, torch.float32), x.device)
+    if not dw.is_contiguous():
+        raise ValueError("out must be contiguous")
+    _call("bakron_matmul_grouped_dw",
+          (dy.data_ptr(), _types()[x.dtype], _ld(dy, 0, n, 8), x.data_ptr(), _ld(x, 0, k, 8), offsets.data_ptr(),
+           experts, dw.data_ptr(), _types()[dw.dtype], rows, n, k), ws, stream, check_status, x.device)
+    return dw
+
+
+def gram_grouped(X, offsets, damping=0.0, *, ws=None, out=None, stream=None, check_status=True):
+    """:func:`gram` for every expert of a layer: ``A[e] = X_e^T X_e / N_e +
+    damping * mean(diag) * I`` from packed samples ``X`` (rows x d, float32,
+    bfloat16 or float16) whose experts' row bounds are ``offsets`` (int32,
+    experts + 1, on the device); experts x d x d float32, zeros for an expert
+    without rows (``bakron_gram_grouped``)."""
+    torch = _torch()
+    _here(X, "X", (2,), tuple(_types()))
+    experts = _groups(offsets)
+    rows, d = X.shape
+    A = _result(out, (experts, d, d), torch.float32, (torch.float32,), X.device)
+    if not A.is_contiguous():
+        raise ValueError("out must be contiguous")
+    t = _types()[X.dtype]
+    need = _lib().bakron_gram_grouped_workspace_size(t, rows, d) if ws is None else 0
+    _call("bakron_gram_grouped", (X.data_ptr(), t, _ld(X, 0, d, 8), offsets.data_ptr(), experts, float(damping),
+                                  A.data_ptr(), rows, d), ws, stream, check_status, X.device, need)
     return A
 
 

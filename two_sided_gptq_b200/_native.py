@@ -99,6 +99,19 @@ SIGNATURES = {
     "bakron_tune_leaf": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, ctypes.POINTER(Quantizer), _vp, _vp, _vp, _vp, _sz,
                                         ctypes.POINTER(Config), _vp, ctypes.POINTER(ctypes.c_int32),
                                         ctypes.POINTER(ctypes.c_double)]),
+    "bakron_quantize_blocks": (ctypes.c_int, [_vp, ctypes.c_int32, _i64, _i64, _i64, _i64, _i64, ctypes.c_int32, _vp,
+                                              _i64, _vp, _vp, _sz, _vp]),
+    "bakron_matmul_blocks": (ctypes.c_int, [_vp, _i64, _vp, _vp, _i64, _i64, _vp, ctypes.c_int32, _vp, _i64, _vp,
+                                            ctypes.c_int32, _i64, _i64, _i64, _i64, _vp, _sz, _vp]),
+    "bakron_matmul_grouped": (ctypes.c_int, [_vp, ctypes.c_int32, _i64, _vp, _i64, _i64, _vp, _i64, _vp,
+                                             ctypes.c_int32, _i64, _i64, _i64, _i64, _vp, _sz, _vp]),
+    "bakron_matmul_grouped_dx": (ctypes.c_int, [_vp, ctypes.c_int32, _i64, _vp, _i64, _i64, _vp, _i64, _vp,
+                                                ctypes.c_int32, _i64, _i64, _i64, _i64, _vp, _sz, _vp]),
+    "bakron_matmul_grouped_dw": (ctypes.c_int, [_vp, ctypes.c_int32, _i64, _vp, _i64, _vp, _i64, _vp, ctypes.c_int32,
+                                                _i64, _i64, _i64, _vp, _sz, _vp]),
+    "bakron_gram_grouped_workspace_size": (_sz, [ctypes.c_int32, _i64, _i64]),
+    "bakron_gram_grouped": (ctypes.c_int, [_vp, ctypes.c_int32, _i64, _vp, _i64, ctypes.c_float, _vp, _i64, _i64, _vp,
+                                           _sz, _vp]),
     "bakron_solve_noalloc": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, ctypes.POINTER(Quantizer), _vp, _vp, _vp,
                                             ctypes.POINTER(Config), _vp, ctypes.POINTER(ctypes.c_int32)]),
 }

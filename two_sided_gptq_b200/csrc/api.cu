@@ -166,6 +166,18 @@ bool env_int(const char *name, int lo, int hi, int &v)
     return true;
 }
 
+}  // namespace
+
+namespace bakron {
+bool default_timeout_ms(int &ms)
+{
+    ms = Config().timeout_ms;
+    return env_int("BAKRON_TIMEOUT_MS", 1, 600000, ms);
+}
+}  // namespace bakron
+
+namespace {
+
 bakron_status_t read_config(const bakron_config_t *c, Config &out)
 {
     out = Config();

@@ -115,6 +115,10 @@ bakron_status_t solve_direct(const float *W, int64_t m, int64_t n, const float *
                              const bakron_quantizer_t *q, float *V, int8_t *codes, float *scales, void *ws,
                              size_t ws_bytes, const bakron_config_t *cfg, cudaStream_t stream);
 
+// The limit of device-side bounded waits where the caller gives none (200 ms,
+// or BAKRON_TIMEOUT_MS); false if that variable is not a valid limit.
+bool default_timeout_ms(int &ms);
+
 // One thread waits on an mbarrier nothing completes, with the band kernel's
 // bounded-wait helper; records BAKRON_ERR_DEVICE_TIMEOUT when it gives up.
 cudaError_t launch_wait_timeout_selftest(DeviceStatus *st, int timeout_ms, cudaStream_t stream);

@@ -1,0 +1,388 @@
+// mm_api.cu -- the C ABI of the products over packed rows and of the 8-bit
+// block quantiser (include/bakron.h): argument checks, tensor maps and the
+// choice of kernel variant.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "kernels.cuh"
+#include "mm.cuh"
+
+using namespace bakron;
+
+using namespace bakron::mm;
+
+namespace {
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+int64_t ceil64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Largest extent of a dimension, tensor-map strides and tile counts.
+constexpr int64_t kMaxDim = (int64_t)1 << 30;
+constexpr int64_t kMaxStride = (int64_t)1 << 39;  // bytes; tensor maps take strides below 2^40
+constexpr int64_t kMaxTiles = (int64_t)1 << 30;
+
+std::mutex g_mu;
+int g_sms[64] = {};  // SM count of each configured device
+
+// Kernel attributes once per device; the device's SM count.
+cudaError_t configure_device(int &sms)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!g_sms[dev]) {
+        int n = 0;
+        if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+        if ((e = configure_rows()) != cudaSuccess) return e;
+        if ((e = configure_eight()) != cudaSuccess) return e;
+        if ((e = configure_outer()) != cudaSuccess) return e;
+        g_sms[dev] = n;
+    }
+    sms = g_sms[dev];
+    return cudaSuccess;
+}
+
+// Status block, cleared before the call's kernels.
+bakron_status_t begin(void *ws, size_t ws_bytes, size_t need, cudaStream_t stream, Args &g)
+{
+    if (!ws || ws_bytes < need) return BAKRON_ERR_WORKSPACE;
+    if (!aligned16(ws)) return BAKRON_ERR_ALIGNMENT;
+    int ms = 0;
+    if (!default_timeout_ms(ms)) return BAKRON_ERR_INVALID_ARG;
+    g.timeout_ns = (uint64_t)ms * 1000000ull;
+    g.st = (DeviceStatus *)ws;
+    if (cudaMemsetAsync(ws, 0, kStatusBytes, stream) != cudaSuccess) return BAKRON_ERR_CUDA;
+    return BAKRON_OK;
+}
+
+bool type16(int32_t t) { return t == BAKRON_BF16 || t == BAKRON_F16; }
+int64_t type_size(int32_t t) { return t == BAKRON_F32 ? 4 : 2; }
+bool dim_ok(int64_t x) { return x >= 1 && x <= kMaxDim; }
+
+// A row-major operand read by TMA: rows of `cols` elements, `stride` elements apart.
+bakron_status_t check_operand(const void *p, int64_t cols, int64_t stride, int64_t size)
+{
+    if (!p || stride < cols) return BAKRON_ERR_INVALID_ARG;
+    if (!aligned16(p) || (stride * size) % 16) return BAKRON_ERR_ALIGNMENT;
+    return stride * size > kMaxStride ? BAKRON_ERR_INVALID_ARG : BAKRON_OK;
+}
+
+// Instruction descriptor without M and N: FP32 accumulator, operand types, transposes.
+uint32_t idesc16(int32_t type, bool a_columns, bool b_columns)
+{
+    const uint32_t t = type == BAKRON_BF16 ? 1u : 0u;
+    return (1u << 4) | (t << 7) | (t << 10) | ((uint32_t)a_columns << 15) | ((uint32_t)b_columns << 16);
+}
+constexpr uint32_t kIdescE4m3 = 1u << 4;
+
+CUtensorMapDataType map_type(int32_t type)
+{
+    return type == BAKRON_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+// Packed rows (rows x cols) / expert matrices (experts x rows x cols).
+bool map2(CUtensorMap *m, CUtensorMapDataType t, int64_t size, const void *p, int64_t cols, int64_t rows,
+          int64_t stride, uint32_t box_cols, uint32_t box_rows)
+{
+    const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)(stride * size)};
+    const uint32_t box[2] = {box_cols, box_rows};
+    return encode_tensor_map(m, t, 2, p, dims, strides, box);
+}
+bool map3(CUtensorMap *m, CUtensorMapDataType t, int64_t size, const void *p, int64_t cols, int64_t rows,
+          int64_t stride, int64_t planes, int64_t plane_stride, uint32_t box_cols, uint32_t box_rows)
+{
+    const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)planes};
+    const uint64_t strides[2] = {(uint64_t)(stride * size), (uint64_t)(plane_stride * size)};
+    const uint32_t box[3] = {box_cols, box_rows, 1};
+    return encode_tensor_map(m, t, 3, p, dims, strides, box);
+}
+
+// Tiles a call can have at most: every group adds at most one partial tile of
+// packed rows, and a group without rows adds none.
+int64_t row_tiles(int64_t rows, int64_t experts, int64_t tile)
+{
+    return rows / tile + (experts < rows ? experts : rows);
+}
+
+// y[t, :] = x[t, :] w_e^T (columns = false: contraction over w's columns) or
+// x[t, :] w_e (columns = true: over w's rows).
+bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t ldx, const void *w, int64_t ldw,
+                             int64_t w_stride, const int32_t *offsets, int64_t experts, void *y, int32_t y_type,
+                             int64_t ldy, int64_t rows, int64_t n, int64_t k, void *ws, size_t ws_bytes,
+                             bakron_stream_t stream)
+{
+    const int64_t in = columns ? n : k, out = columns ? k : n;  // widths of x and y
+    if (rows < 0 || rows > kMaxDim || !dim_ok(n) || !dim_ok(k) || experts < 1 || experts > kMaxExperts)
+        return BAKRON_ERR_INVALID_ARG;
+    if (!type16(type) || (y_type != type && y_type != BAKRON_F32) || !offsets) return BAKRON_ERR_INVALID_ARG;
+    if (((uintptr_t)offsets & 3u) || w_stride < n * ldw) return BAKRON_ERR_INVALID_ARG;
+    bakron_status_t s = check_operand(w, k, ldw, 2);
+    if (s == BAKRON_OK && w_stride * 2 > kMaxStride) s = BAKRON_ERR_INVALID_ARG;
+    if (s == BAKRON_OK && (w_stride * 2) % 16) s = BAKRON_ERR_ALIGNMENT;
+    if (s == BAKRON_OK && rows) s = check_operand(x, in, ldx, 2);
+    if (s != BAKRON_OK) return s;
+    if (rows && (!y || ldy < out)) return BAKRON_ERR_INVALID_ARG;
+    if (rows && !aligned16(y)) return BAKRON_ERR_ALIGNMENT;
+    // Tiles of 64 packed rows when the groups are short on average: the same
+    // weight tile then takes half the stage bytes, so twice the weights are in
+    // flight.
+    const bool small = rows <= 48 * experts;
+    const int64_t bn = small ? 64 : 256;
+    const int64_t tiles = row_tiles(rows, experts, bn) * ceil64(out, 128);
+    if (tiles > kMaxTiles) return BAKRON_ERR_INVALID_ARG;
+    int sms = 0;
+    if (configure_device(sms) != cudaSuccess) return BAKRON_ERR_CUDA;
+    Args g{};
+    if ((s = begin(ws, ws_bytes, kStatusBytes, (cudaStream_t)stream, g)) != BAKRON_OK) return s;
+    if (!rows) return BAKRON_OK;
+    g.offsets = offsets;
+    g.experts = (int)experts;
+    g.rows = (int)rows;
+    g.a_total = (int)out;
+    g.k_total = (int)in;
+    g.out = y;
+    g.ldo = ldy;
+    g.out_type = y_type;
+    g.idesc = idesc16(type, columns, false);
+    Maps m;
+    const CUtensorMapDataType t = map_type(type);
+    if (!map3(&m.a, t, 2, w, k, n, ldw, experts, w_stride, 64, columns ? 64 : 128) ||
+        !map2(&m.b, t, 2, x, in, rows, ldx, 64, small ? 32 : 64))
+        return BAKRON_ERR_CUDA;
+    const Variant v = columns ? (small ? kRowsDx64 : kRowsDx256) : (small ? kRows64 : kRows256);
+    if (launch_rows(v, m, g, (int)min64(tiles, sms), (cudaStream_t)stream) != cudaSuccess) return BAKRON_ERR_CUDA;
+    return BAKRON_OK;
+}
+
+struct GramGroupedLayout {
+    int64_t ld;
+    size_t status, planes, total;
+    void compute(int32_t type, int64_t rows, int64_t d)
+    {
+        ld = ceil64(d, 8) * 8;
+        status = 0;
+        planes = kAlign;
+        total = align_up(planes + (type == BAKRON_F32 ? (size_t)3 * rows * ld * 2 : 0));
+    }
+};
+
+}  // namespace
+
+extern "C" {
+
+bakron_status_t bakron_quantize_blocks(const void *x_dev, int32_t x_type, int64_t batch, int64_t rows, int64_t cols,
+                                       int64_t x_batch_stride, int64_t x_row_stride, int32_t block_rows,
+                                       uint8_t *q_dev, int64_t q_row_stride, float *scales_dev, void *ws_dev,
+                                       size_t ws_bytes, bakron_stream_t stream)
+{
+    if (batch < 0 || rows < 0 || batch > kMaxDim || rows > kMaxDim || !dim_ok(cols)) return BAKRON_ERR_INVALID_ARG;
+    if (x_type != BAKRON_F32 && !type16(x_type)) return BAKRON_ERR_INVALID_ARG;
+    if (block_rows != 1 && block_rows != 128) return BAKRON_ERR_INVALID_ARG;
+    if (x_row_stride < cols || q_row_stride < cols || x_batch_stride < 0) return BAKRON_ERR_INVALID_ARG;
+    if (batch * ceil64(rows, block_rows) > kMaxDim) return BAKRON_ERR_INVALID_ARG;
+    const int64_t blocks = batch * ceil64(rows, block_rows) * ceil64(cols, 128);
+    if (block_rows == 128 && blocks > kMaxTiles) return BAKRON_ERR_INVALID_ARG;
+    if (blocks && (!x_dev || !q_dev || !scales_dev)) return BAKRON_ERR_INVALID_ARG;
+    if (!aligned16(x_dev) || !aligned16(q_dev) || !aligned16(scales_dev) || q_row_stride % 16)
+        return BAKRON_ERR_ALIGNMENT;
+    Args g{};
+    const bakron_status_t s = begin(ws_dev, ws_bytes, kStatusBytes, (cudaStream_t)stream, g);
+    if (s != BAKRON_OK || !blocks) return s;
+    const QuantArgs a{x_dev, x_type, batch, rows, cols, x_batch_stride, x_row_stride, block_rows,
+                      q_dev, q_row_stride, scales_dev, g.st};
+    return launch_quantize(a, (cudaStream_t)stream) == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA;
+}
+
+bakron_status_t bakron_matmul_blocks(const uint8_t *x_dev, int64_t x_row_stride, const float *x_scales_dev,
+                                     const uint8_t *w_dev, int64_t w_row_stride, int64_t w_expert_stride,
+                                     const float *w_scales_dev, int32_t w_scale_rows, const int32_t *offsets_dev,
+                                     int64_t experts, void *y_dev, int32_t y_type, int64_t y_row_stride, int64_t rows,
+                                     int64_t n, int64_t k, void *ws_dev, size_t ws_bytes, bakron_stream_t stream)
+{
+    if (rows < 0 || rows > kMaxDim || !dim_ok(n) || !dim_ok(k) || experts < 1 || experts > kMaxExperts)
+        return BAKRON_ERR_INVALID_ARG;
+    if (!offsets_dev && experts != 1) return BAKRON_ERR_INVALID_ARG;
+    if (y_type != BAKRON_F32 && !type16(y_type)) return BAKRON_ERR_INVALID_ARG;
+    if (w_scale_rows != 1 && w_scale_rows != 128) return BAKRON_ERR_INVALID_ARG;
+    if (!w_scales_dev || ((uintptr_t)offsets_dev & 3u) || w_expert_stride < n * w_row_stride)
+        return BAKRON_ERR_INVALID_ARG;
+    bakron_status_t s = check_operand(w_dev, k, w_row_stride, 1);
+    if (s == BAKRON_OK && w_expert_stride > kMaxStride) s = BAKRON_ERR_INVALID_ARG;
+    if (s == BAKRON_OK && w_expert_stride % 16) s = BAKRON_ERR_ALIGNMENT;
+    if (s == BAKRON_OK && rows) s = check_operand(x_dev, k, x_row_stride, 1);
+    if (s != BAKRON_OK) return s;
+    if (rows && (!x_scales_dev || !y_dev || y_row_stride < n)) return BAKRON_ERR_INVALID_ARG;
+    if (!aligned16(w_scales_dev) || (rows && (!aligned16(y_dev) || !aligned16(x_scales_dev))))
+        return BAKRON_ERR_ALIGNMENT;
+    // Packed rows on the tile's columns (64 at a time) while the groups are
+    // short, on its 128 rows beyond that.
+    const bool small = rows <= 64 * experts;
+    const int64_t tiles = small ? row_tiles(rows, experts, 64) * ceil64(n, 128)
+                                : row_tiles(rows, experts, 128) * ceil64(n, 256);
+    if (tiles > kMaxTiles) return BAKRON_ERR_INVALID_ARG;
+    int sms = 0;
+    if (configure_device(sms) != cudaSuccess) return BAKRON_ERR_CUDA;
+    Args g{};
+    if ((s = begin(ws_dev, ws_bytes, kStatusBytes, (cudaStream_t)stream, g)) != BAKRON_OK) return s;
+    if (!rows) return BAKRON_OK;
+    g.offsets = offsets_dev;
+    g.experts = (int)experts;
+    g.rows = (int)rows;
+    g.a_total = (int)n;
+    g.b_total = (int)n;
+    g.k_total = (int)k;
+    g.out = y_dev;
+    g.ldo = y_row_stride;
+    g.out_type = y_type;
+    g.idesc = kIdescE4m3;
+    g.x_steps = x_scales_dev;
+    g.w_steps = w_scales_dev;
+    g.w_step_rows = w_scale_rows;
+    Maps m;
+    const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    CUtensorMap *xm = small ? &m.b : &m.a, *wm = small ? &m.a : &m.b;
+    if (!map2(xm, t, 1, x_dev, k, rows, x_row_stride, 128, small ? 32 : 128) ||
+        !map3(wm, t, 1, w_dev, k, n, w_row_stride, experts, w_expert_stride, 128, small ? 128 : 256))
+        return BAKRON_ERR_CUDA;
+    if (launch_eight(small ? kEightB64 : kEightA256, m, g, (int)min64(tiles, sms), (cudaStream_t)stream) !=
+        cudaSuccess)
+        return BAKRON_ERR_CUDA;
+    return BAKRON_OK;
+}
+
+bakron_status_t bakron_matmul_grouped(const void *x_dev, int32_t type, int64_t x_row_stride, const void *w_dev,
+                                      int64_t w_row_stride, int64_t w_expert_stride, const int32_t *offsets_dev,
+                                      int64_t experts, void *y_dev, int32_t y_type, int64_t y_row_stride, int64_t rows,
+                                      int64_t n, int64_t k, void *ws_dev, size_t ws_bytes, bakron_stream_t stream)
+{
+    return grouped_rows(false, x_dev, type, x_row_stride, w_dev, w_row_stride, w_expert_stride, offsets_dev, experts,
+                        y_dev, y_type, y_row_stride, rows, n, k, ws_dev, ws_bytes, stream);
+}
+
+bakron_status_t bakron_matmul_grouped_dx(const void *dy_dev, int32_t type, int64_t dy_row_stride, const void *w_dev,
+                                         int64_t w_row_stride, int64_t w_expert_stride, const int32_t *offsets_dev,
+                                         int64_t experts, void *dx_dev, int32_t dx_type, int64_t dx_row_stride,
+                                         int64_t rows, int64_t n, int64_t k, void *ws_dev, size_t ws_bytes,
+                                         bakron_stream_t stream)
+{
+    return grouped_rows(true, dy_dev, type, dy_row_stride, w_dev, w_row_stride, w_expert_stride, offsets_dev, experts,
+                        dx_dev, dx_type, dx_row_stride, rows, n, k, ws_dev, ws_bytes, stream);
+}
+
+bakron_status_t bakron_matmul_grouped_dw(const void *dy_dev, int32_t type, int64_t dy_row_stride, const void *x_dev,
+                                         int64_t x_row_stride, const int32_t *offsets_dev, int64_t experts,
+                                         void *dw_dev, int32_t dw_type, int64_t rows, int64_t n, int64_t k,
+                                         void *ws_dev, size_t ws_bytes, bakron_stream_t stream)
+{
+    if (rows < 0 || rows > kMaxDim || !dim_ok(n) || !dim_ok(k) || experts < 1 || experts > kMaxExperts)
+        return BAKRON_ERR_INVALID_ARG;
+    if (!type16(type) || (dw_type != type && dw_type != BAKRON_F32) || !offsets_dev || !dw_dev)
+        return BAKRON_ERR_INVALID_ARG;
+    if ((uintptr_t)offsets_dev & 3u) return BAKRON_ERR_INVALID_ARG;
+    bakron_status_t s = BAKRON_OK;
+    if (rows) s = check_operand(dy_dev, n, dy_row_stride, 2);
+    if (s == BAKRON_OK && rows) s = check_operand(x_dev, k, x_row_stride, 2);
+    if (s != BAKRON_OK) return s;
+    if (!aligned16(dw_dev)) return BAKRON_ERR_ALIGNMENT;
+    const int64_t tiles = experts * ceil64(n, 128) * ceil64(k, 256);
+    if (tiles > kMaxTiles) return BAKRON_ERR_INVALID_ARG;
+    int sms = 0;
+    if (configure_device(sms) != cudaSuccess) return BAKRON_ERR_CUDA;
+    Args g{};
+    if ((s = begin(ws_dev, ws_bytes, kStatusBytes, (cudaStream_t)stream, g)) != BAKRON_OK) return s;
+    if (!rows) {
+        const size_t bytes = (size_t)experts * n * k * type_size(dw_type);
+        return cudaMemsetAsync(dw_dev, 0, bytes, (cudaStream_t)stream) == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA;
+    }
+    g.offsets = offsets_dev;
+    g.experts = (int)experts;
+    g.rows = (int)rows;
+    g.a_total = (int)n;
+    g.b_total = (int)k;
+    g.out = dw_dev;
+    g.ldo = k;
+    g.out_expert_stride = n * k;
+    g.out_type = dw_type;
+    g.idesc = idesc16(type, true, true);
+    Maps m;
+    const CUtensorMapDataType t = map_type(type);
+    if (!map3(&m.a, t, 2, dy_dev, n, rows, dy_row_stride, 1, rows * dy_row_stride, 64, 64) ||
+        !map3(&m.b, t, 2, x_dev, k, rows, x_row_stride, 1, rows * x_row_stride, 64, 64))
+        return BAKRON_ERR_CUDA;
+    if (launch_outer(kOuter, m, g, (int)min64(tiles, sms), (cudaStream_t)stream) != cudaSuccess)
+        return BAKRON_ERR_CUDA;
+    return BAKRON_OK;
+}
+
+size_t bakron_gram_grouped_workspace_size(int32_t type, int64_t rows, int64_t d)
+{
+    if ((type != BAKRON_F32 && !type16(type)) || rows < 0 || rows > kMaxDim || !dim_ok(d)) return 0;
+    GramGroupedLayout L;
+    L.compute(type, rows, d);
+    return L.total;
+}
+
+bakron_status_t bakron_gram_grouped(const void *X_dev, int32_t type, int64_t x_row_stride, const int32_t *offsets_dev,
+                                    int64_t experts, float damping, float *A_dev, int64_t rows, int64_t d,
+                                    void *ws_dev, size_t ws_bytes, bakron_stream_t stream)
+{
+    if (rows < 0 || rows > kMaxDim || !dim_ok(d) || experts < 1 || experts > kMaxExperts)
+        return BAKRON_ERR_INVALID_ARG;
+    if ((type != BAKRON_F32 && !type16(type)) || !offsets_dev || !A_dev || ((uintptr_t)offsets_dev & 3u))
+        return BAKRON_ERR_INVALID_ARG;
+    if (!(damping >= 0.f) || !isfinite(damping)) return BAKRON_ERR_INVALID_ARG;
+    bakron_status_t s = BAKRON_OK;
+    if (rows && type == BAKRON_F32) {
+        // read by plain loads: any row stride
+        if (!X_dev || x_row_stride < d) return BAKRON_ERR_INVALID_ARG;
+        if (!aligned16(X_dev)) return BAKRON_ERR_ALIGNMENT;
+    } else if (rows) {
+        s = check_operand(X_dev, d, x_row_stride, 2);
+    }
+    if (s != BAKRON_OK) return s;
+    if (!aligned16(A_dev)) return BAKRON_ERR_ALIGNMENT;
+    const int64_t mt = ceil64(d, 128), tiles = experts * (mt * (mt + 1) / 2);
+    if (mt > 16384 || tiles > kMaxTiles) return BAKRON_ERR_INVALID_ARG;
+    GramGroupedLayout L;
+    L.compute(type, rows, d);
+    int sms = 0;
+    if (configure_device(sms) != cudaSuccess) return BAKRON_ERR_CUDA;
+    cudaStream_t st = (cudaStream_t)stream;
+    Args g{};
+    if ((s = begin(ws_dev, ws_bytes, L.total, st, g)) != BAKRON_OK) return s;
+    if (!rows)
+        return cudaMemsetAsync(A_dev, 0, (size_t)experts * d * d * 4, st) == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA;
+    g.offsets = offsets_dev;
+    g.experts = (int)experts;
+    g.rows = (int)rows;
+    g.a_total = (int)d;
+    g.b_total = (int)d;
+    g.out = A_dev;
+    g.ldo = d;
+    g.out_expert_stride = d * d;
+    g.out_type = BAKRON_F32;
+    Maps m;
+    if (type == BAKRON_F32) {
+        uint16_t *planes = (uint16_t *)((char *)ws_dev + L.planes);
+        if (launch_split_three((const float *)X_dev, rows, d, x_row_stride, planes, L.ld, st) != cudaSuccess)
+            return BAKRON_ERR_CUDA;
+        g.idesc = idesc16(BAKRON_BF16, true, true);
+        if (!map3(&m.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, planes, d, rows, L.ld, 3, rows * L.ld, 64, 32))
+            return BAKRON_ERR_CUDA;
+    } else {
+        g.idesc = idesc16(type, true, true);
+        if (!map3(&m.a, map_type(type), 2, X_dev, d, rows, x_row_stride, 1, rows * x_row_stride, 64, 64))
+            return BAKRON_ERR_CUDA;
+    }
+    m.b = m.a;
+    if (launch_outer(type == BAKRON_F32 ? kGramThree : kGramOne, m, g, (int)min64(tiles, sms), st) != cudaSuccess)
+        return BAKRON_ERR_CUDA;
+    return launch_gram_damp(A_dev, d, (int)experts, damping, g.st, st) == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,109 @@
+// mm_outer.cu -- products whose contraction is the packed rows of a group: the
+// experts' weight gradients dw_e = dy_e^T x_e, and one Gram factor per expert,
+// A_e = X_e^T X_e / N_e + damping * mean(diag) * I (the K-FAC factor of an
+// expert's inputs or output gradients, "Assumptions & free parameters": Gram
+// matrix regularisation).
+//
+// FP32 samples are split once into three bf16 parts, x = h + m + l to 2^-27 of
+// x; the products hh + (hm + mh) + mm + (hl + lh) on the bf16 tensor cores cost
+// what three TF32 products would and keep 24 bits instead of 21.
+#include "mm_kernel.cuh"
+
+namespace bakron {
+namespace mm {
+
+namespace {
+struct Outer {
+    static constexpr Ragged kRagged = kContract;
+    static constexpr bool kEight = false, kAColumns = true, kLower = false;
+    static constexpr int kBN = 256, kPlanes = 1, kChunk = 4, kKRows = 64, kBoxRows = 64;
+};
+template <int Planes>
+struct Gram {
+    static constexpr Ragged kRagged = kContract;
+    static constexpr bool kEight = false, kAColumns = true, kLower = true;
+    static constexpr int kBN = 128, kPlanes = Planes, kChunk = 4, kKRows = Planes > 1 ? 32 : 64, kBoxRows = kKRows;
+};
+
+// Three bf16 parts of an fp32 matrix, each rounded to nearest from what the
+// earlier ones leave (those differences are exact in fp32).
+__global__ void split_three_kernel(const float *__restrict__ x, int64_t rows, int64_t d, int64_t ldx,
+                                   __nv_bfloat16 *__restrict__ out, int64_t ld)
+{
+    const int64_t plane = rows * ld, n = rows * d;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t r = i / d, c = i - r * d;
+        const float v = x[r * ldx + c];
+        const __nv_bfloat16 h = __float2bfloat16_rn(v);
+        const float r1 = v - __bfloat162float(h);
+        const __nv_bfloat16 m = __float2bfloat16_rn(r1);
+        __nv_bfloat16 *o = out + r * ld + c;
+        o[0] = h;
+        o[plane] = m;
+        o[2 * plane] = __float2bfloat16_rn(r1 - __bfloat162float(m));
+    }
+}
+
+// One CTA per group: the mean of the diagonal (FP64, a fixed order), then
+// damping times it on the diagonal.  A diagonal entry is a sum of squares, so
+// it is NaN or infinite whenever the group's samples hold such a value (or
+// their squares overflow): recorded as BAKRON_ERR_NONFINITE.
+__global__ void gram_damp_kernel(float *__restrict__ A, int64_t d, float damping, DeviceStatus *st)
+{
+    __shared__ double part[32];
+    __shared__ float add_sh;
+    float *a = A + (int64_t)blockIdx.x * d * d;
+    double sum = 0.0;
+    bool finite = true;
+    for (int64_t i = threadIdx.x; i < d; i += blockDim.x) {
+        const float v = a[i * d + i];
+        finite &= isfinite(v);
+        sum += (double)v;
+    }
+    if (!finite) record_error(st, BAKRON_ERR_NONFINITE, (int)blockIdx.x);
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double t = 0.0;
+        for (int w = 0; w < (int)(blockDim.x >> 5); ++w) t += part[w];
+        add_sh = (float)((double)damping * (t / (double)d));
+    }
+    __syncthreads();
+    const float add = add_sh;
+    for (int64_t i = threadIdx.x; i < d; i += blockDim.x) a[i * d + i] = __fadd_rn(a[i * d + i], add);
+}
+}  // namespace
+
+cudaError_t configure_outer()
+{
+    cudaError_t e = configure<Outer>();
+    if (e == cudaSuccess) e = configure<Gram<1>>();
+    return e == cudaSuccess ? configure<Gram<3>>() : e;
+}
+
+cudaError_t launch_outer(Variant v, const Maps &maps, const Args &g, int blocks, cudaStream_t stream)
+{
+    switch (v) {
+    case kOuter: return launch<Outer>(maps, g, blocks, stream);
+    case kGramOne: return launch<Gram<1>>(maps, g, blocks, stream);
+    default: return launch<Gram<3>>(maps, g, blocks, stream);
+    }
+}
+
+cudaError_t launch_split_three(const float *x, int64_t rows, int64_t d, int64_t ldx, uint16_t *planes, int64_t ld,
+                               cudaStream_t stream)
+{
+    const int64_t blocks = min64((rows * d + 1023) / 1024, 148 * 8);
+    split_three_kernel<<<(unsigned)blocks, 256, 0, stream>>>(x, rows, d, ldx, (__nv_bfloat16 *)planes, ld);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gram_damp(float *A, int64_t d, int experts, float damping, DeviceStatus *st, cudaStream_t stream)
+{
+    gram_damp_kernel<<<experts, 256, 0, stream>>>(A, d, damping, st);
+    return cudaGetLastError();
+}
+
+}  // namespace mm
+}  // namespace bakron
