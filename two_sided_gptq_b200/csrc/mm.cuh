@@ -44,9 +44,12 @@ enum Variant {
 cudaError_t configure_rows();
 cudaError_t configure_eight();
 cudaError_t configure_outer();
-cudaError_t launch_rows(Variant v, const Maps &maps, const Args &g, int blocks, cudaStream_t stream);
-cudaError_t launch_eight(Variant v, const Maps &maps, const Args &g, int blocks, cudaStream_t stream);
-cudaError_t launch_outer(Variant v, const Maps &maps, const Args &g, int blocks, cudaStream_t stream);
+cudaError_t launch_rows(Variant v, const Maps &maps, const Args &g, int64_t tiles, int sms,
+                        cudaStream_t stream);
+cudaError_t launch_eight(Variant v, const Maps &maps, const Args &g, int64_t tiles, int sms,
+                        cudaStream_t stream);
+cudaError_t launch_outer(Variant v, const Maps &maps, const Args &g, int64_t tiles, int sms,
+                        cudaStream_t stream);
 
 // x ~= h + m + l in bf16, three planes of rows x ld; fp32 input with row stride ldx.
 cudaError_t launch_split_three(const float *x, int64_t rows, int64_t d, int64_t ldx, uint16_t *planes, int64_t ld,

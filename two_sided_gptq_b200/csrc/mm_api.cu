@@ -155,7 +155,7 @@ bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t 
         !map2(&m.b, t, 2, x, in, rows, ldx, 64, small ? 32 : 64))
         return BAKRON_ERR_CUDA;
     const Variant v = columns ? (small ? kRowsDx64 : kRowsDx256) : (small ? kRows64 : kRows256);
-    if (launch_rows(v, m, g, (int)min64(tiles, sms), (cudaStream_t)stream) != cudaSuccess) return BAKRON_ERR_CUDA;
+    if (launch_rows(v, m, g, tiles, sms, (cudaStream_t)stream) != cudaSuccess) return BAKRON_ERR_CUDA;
     return BAKRON_OK;
 }
 
@@ -247,9 +247,9 @@ bakron_status_t bakron_matmul_blocks(const uint8_t *x_dev, int64_t x_row_stride,
     const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     CUtensorMap *xm = small ? &m.b : &m.a, *wm = small ? &m.a : &m.b;
     if (!map2(xm, t, 1, x_dev, k, rows, x_row_stride, 128, small ? 32 : 128) ||
-        !map3(wm, t, 1, w_dev, k, n, w_row_stride, experts, w_expert_stride, 128, small ? 128 : 256))
+        !map3(wm, t, 1, w_dev, k, n, w_row_stride, experts, w_expert_stride, 128, 128))
         return BAKRON_ERR_CUDA;
-    if (launch_eight(small ? kEightB64 : kEightA256, m, g, (int)min64(tiles, sms), (cudaStream_t)stream) !=
+    if (launch_eight(small ? kEightB64 : kEightA256, m, g, tiles, sms, (cudaStream_t)stream) !=
         cudaSuccess)
         return BAKRON_ERR_CUDA;
     return BAKRON_OK;
@@ -314,7 +314,7 @@ bakron_status_t bakron_matmul_grouped_dw(const void *dy_dev, int32_t type, int64
     if (!map3(&m.a, t, 2, dy_dev, n, rows, dy_row_stride, 1, rows * dy_row_stride, 64, 64) ||
         !map3(&m.b, t, 2, x_dev, k, rows, x_row_stride, 1, rows * x_row_stride, 64, 64))
         return BAKRON_ERR_CUDA;
-    if (launch_outer(kOuter, m, g, (int)min64(tiles, sms), (cudaStream_t)stream) != cudaSuccess)
+    if (launch_outer(kOuter, m, g, tiles, sms, (cudaStream_t)stream) != cudaSuccess)
         return BAKRON_ERR_CUDA;
     return BAKRON_OK;
 }
@@ -380,7 +380,7 @@ bakron_status_t bakron_gram_grouped(const void *X_dev, int32_t type, int64_t x_r
             return BAKRON_ERR_CUDA;
     }
     m.b = m.a;
-    if (launch_outer(type == BAKRON_F32 ? kGramThree : kGramOne, m, g, (int)min64(tiles, sms), st) != cudaSuccess)
+    if (launch_outer(type == BAKRON_F32 ? kGramThree : kGramOne, m, g, tiles, sms, st) != cudaSuccess)
         return BAKRON_ERR_CUDA;
     return launch_gram_damp(A_dev, d, (int)experts, damping, g.st, st) == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA;
 }

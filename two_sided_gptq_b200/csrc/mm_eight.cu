@@ -12,12 +12,12 @@ namespace mm {
 namespace {
 struct EightA {
     static constexpr Ragged kRagged = kTokensA;
-    static constexpr bool kEight = true, kAColumns = false, kLower = false;
+    static constexpr bool kPair = true, kEight = true, kAColumns = false, kLower = false;
     static constexpr int kBN = 256, kPlanes = 1, kChunk = 1, kKRows = 0, kBoxRows = 128;
 };
 struct EightB {
     static constexpr Ragged kRagged = kTokensB;
-    static constexpr bool kEight = true, kAColumns = false, kLower = false;
+    static constexpr bool kPair = false, kEight = true, kAColumns = false, kLower = false;
     static constexpr int kBN = 64, kPlanes = 1, kChunk = 1, kKRows = 0, kBoxRows = 32;
 };
 }  // namespace
@@ -28,9 +28,10 @@ cudaError_t configure_eight()
     return e == cudaSuccess ? configure<EightB>() : e;
 }
 
-cudaError_t launch_eight(Variant v, const Maps &maps, const Args &g, int blocks, cudaStream_t stream)
+cudaError_t launch_eight(Variant v, const Maps &maps, const Args &g, int64_t tiles, int sms,
+                        cudaStream_t stream)
 {
-    return v == kEightA256 ? launch<EightA>(maps, g, blocks, stream) : launch<EightB>(maps, g, blocks, stream);
+    return v == kEightA256 ? launch<EightA>(maps, g, tiles, sms, stream) : launch<EightB>(maps, g, tiles, sms, stream);
 }
 
 }  // namespace mm

@@ -18,11 +18,18 @@
 // group offsets in device memory (no host round trip) and takes tiles
 // blockIdx.x, blockIdx.x + gridDim.x, ...
 //
+// With kPair two CTAs of a cluster share one MMA of 256 rows: each holds half
+// of A's, B's and D's rows, so an operand byte brought into shared memory feeds
+// twice the multiply-adds; the pair's first CTA issues the MMAs, and both CTAs'
+// loads complete on its barriers.
+//
 // Warp roles: warp 0 lane 0 issues TMA into a ring of kStages stages; warp 1
-// owns TMEM and issues the MMAs; the other warps read finished accumulator
-// chunks (kChunk stages each, double buffered in TMEM) and add them in FP32
-// registers, scaled by the 8-bit operands' steps where there are any.  The
-// tensor cores' accumulator truncates, so sums are kept to kChunk stages there.
+// owns TMEM and issues the MMAs; warps 4..11 read finished accumulator chunks
+// (kChunk stages each, double buffered in TMEM) and add them in FP32 registers,
+// scaled by the 8-bit operands' steps where there are any.  The tensor cores'
+// accumulator truncates, so sums are kept to kChunk stages there.  Where the
+// packed rows are the contraction, warp 3 zeroes what a group's last stage
+// holds beyond the group.
 // Every mbarrier wait is bounded; on expiry the CTA records
 // BAKRON_ERR_DEVICE_TIMEOUT, drains what it issued, frees its tensor memory and
 // exits.
@@ -45,18 +52,27 @@ constexpr int kReserve = 9 * 1024;  // barriers, tile numbering, alignment, stag
 
 template <class P>
 struct Shape {
+    static constexpr int kCtas = P::kPair ? 2 : 1;
+    static constexpr int kM = kBM * kCtas;                          // D rows of a tile
+    static constexpr int kBRows = P::kBN / kCtas;                   // B rows in one CTA
     // one operand row of a stage is 128 bytes (the swizzle width)
     static constexpr int kElems = P::kEight ? 128 : 64;             // operand elements in 128 bytes
     static constexpr int kKB = P::kRagged == kContract ? P::kKRows : kElems;  // contraction per stage
     static constexpr int kABytes = P::kRagged == kContract ? kBM / 64 * kKB * 128 : kBM * 128;
-    static constexpr int kBBytes = P::kRagged == kContract ? P::kBN / 64 * kKB * 128 : P::kBN * 128;
+    static constexpr int kBBytes = P::kRagged == kContract ? kBRows / 64 * kKB * 128 : kBRows * 128;
     static constexpr int kStageBytes = P::kPlanes * (kABytes + kBBytes);
     static constexpr int kStages = (227 * 1024 - kReserve) / kStageBytes < 8 ? (227 * 1024 - kReserve) / kStageBytes : 8;
     static constexpr int kAcc = P::kPlanes > 1 ? 2 : 1;             // accumulators per buffer
     static constexpr int kTmemCols = 2 * kAcc * P::kBN;
     static constexpr int kEpiWarps = 8;
-    static constexpr int kThreads = 64 + 32 * kEpiWarps;
+    static constexpr int kThreads = 128 + 32 * kEpiWarps;
     static constexpr int kCols = P::kBN / (kEpiWarps / 4);          // columns per epilogue thread
+    // registers: the epilogue's accumulators and two loads in flight need more
+    // than a 12-warp CTA's even share (168), the other warps far less
+    static constexpr bool kSplitRegs = kCols > 64;
+    static constexpr int kRegsOthers = 56, kRegsEpilogue = 224;
+    // a warpgroup can only take registers that the block was launched with
+    static constexpr int kRegsNeeded = 128 * kRegsOthers + 32 * kEpiWarps * kRegsEpilogue;
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kReserve;
 };
 
@@ -83,29 +99,31 @@ __device__ __forceinline__ bool group_range(const Args &g, int e, int &lo, int &
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Lower-triangle tiles of a square of `rows` 128-row tiles by BN columns.
-template <int BN>
+// Tiles of tile row i that reach on or below the diagonal of a square result.
+template <class P>
 __host__ __device__ __forceinline__ int lower_tiles_of_row(int i)
 {
-    return (i * kBM + kBM - 1) / BN + 1;
+    return (i * Shape<P>::kM + Shape<P>::kM - 1) / P::kBN + 1;
 }
 
 template <class P>
 __device__ __forceinline__ int tiles_of_group(const Args &g, int len)
 {
-    if (P::kRagged == kTokensB) return ceil_div(g.a_total, kBM) * ceil_div(len, P::kBN);
-    if (P::kRagged == kTokensA) return ceil_div(len, kBM) * ceil_div(g.b_total, P::kBN);
+    constexpr int kM = Shape<P>::kM;
+    if (P::kRagged == kTokensB) return ceil_div(g.a_total, kM) * ceil_div(len, P::kBN);
+    if (P::kRagged == kTokensA) return ceil_div(len, kM) * ceil_div(g.b_total, P::kBN);
     if (P::kLower) {
         int n = 0;
-        for (int i = 0; i < ceil_div(g.a_total, kBM); ++i) n += lower_tiles_of_row<P::kBN>(i);
+        for (int i = 0; i < ceil_div(g.a_total, kM); ++i) n += lower_tiles_of_row<P>(i);
         return n;
     }
-    return ceil_div(g.a_total, kBM) * ceil_div(g.b_total, P::kBN);
+    return ceil_div(g.a_total, kM) * ceil_div(g.b_total, P::kBN);
 }
 
 template <class P>
 __device__ __forceinline__ Tile find_tile(const Args &g, const int *first, int t)
 {
+    constexpr int kM = Shape<P>::kM;
     int a = 0, b = g.experts;  // the last group whose first tile is <= t
     while (b - a > 1) {
         const int m = (a + b) >> 1;
@@ -119,34 +137,34 @@ __device__ __forceinline__ Tile find_tile(const Args &g, const int *first, int t
     int i = t - first[a];
     x.count = hi - lo;
     if (P::kRagged == kTokensB) {
-        const int mt = ceil_div(g.a_total, kBM);
-        x.a0 = (i % mt) * kBM;
+        const int mt = ceil_div(g.a_total, kM);
+        x.a0 = (i % mt) * kM;
         x.b0 = lo + (i / mt) * P::kBN;
-        x.na = min(kBM, g.a_total - x.a0);
+        x.na = min(kM, g.a_total - x.a0);
         x.nb = min(P::kBN, hi - x.b0);
         x.k0 = 0;
         x.k1 = g.k_total;
     } else if (P::kRagged == kTokensA) {
-        const int mt = ceil_div(hi - lo, kBM);
-        x.a0 = lo + (i % mt) * kBM;
+        const int mt = ceil_div(hi - lo, kM);
+        x.a0 = lo + (i % mt) * kM;
         x.b0 = (i / mt) * P::kBN;
-        x.na = min(kBM, hi - x.a0);
+        x.na = min(kM, hi - x.a0);
         x.nb = min(P::kBN, g.b_total - x.b0);
         x.k0 = 0;
         x.k1 = g.k_total;
     } else {
         int r, c;
         if (P::kLower) {
-            for (r = 0; i >= lower_tiles_of_row<P::kBN>(r); ++r) i -= lower_tiles_of_row<P::kBN>(r);
+            for (r = 0; i >= lower_tiles_of_row<P>(r); ++r) i -= lower_tiles_of_row<P>(r);
             c = i;
         } else {
             const int nt = ceil_div(g.b_total, P::kBN);
             r = i / nt;
             c = i % nt;
         }
-        x.a0 = r * kBM;
+        x.a0 = r * kM;
         x.b0 = c * P::kBN;
-        x.na = min(kBM, g.a_total - x.a0);
+        x.na = min(kM, g.a_total - x.a0);
         x.nb = min(P::kBN, g.b_total - x.b0);
         x.k0 = lo;
         x.k1 = hi;
@@ -163,50 +181,81 @@ __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half round_to<__half>(float v) { return __float2half_rn(v); }
 
-// Store this thread's accumulators: D row `lane_row` of the tile, columns
-// [col0, col0 + C).
-template <class P, typename T, int C>
-__device__ __forceinline__ void store_tile(const Args &g, const Tile &x, int lane_row, int col0, const float (&acc)[C])
+__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8])
 {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+template <typename T>
+__device__ __forceinline__ uint32_t word_of(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t word_of<__nv_bfloat16>(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *(const uint32_t *)&v;
+}
+template <>
+__device__ __forceinline__ uint32_t word_of<__half>(float lo, float hi)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *(const uint32_t *)&v;
+}
+
+// Store this thread's accumulators: D row `lane_row` of the tile, columns
+// [col0, col0 + 2 N).
+template <class P, typename T, int N>
+__device__ __forceinline__ void store_tile(const Args &g, const Tile &x, int lane_row, int col0,
+                                           const uint64_t (&acc)[N])
+{
+    constexpr int C = 2 * N;
     T *out = (T *)g.out;
+    if (lane_row >= x.na) return;
     if (P::kRagged == kTokensB) {
         // D row = output column: the 32 lanes of a warp write consecutive
         // elements of one packed row
-        if (lane_row >= x.na) return;
         T *p = out + (int64_t)(x.b0 + col0) * g.ldo + x.a0 + lane_row;
         float s = 1.f;
         if (P::kEight && g.w_step_rows == 1) s = __ldg(g.w_steps + (int64_t)x.e * g.a_total + x.a0 + lane_row);
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            if (col0 + c < x.nb) p[(int64_t)c * g.ldo] = round_to<T>(P::kEight ? acc[c] * s : acc[c]);
+            if (col0 + c < x.nb) {
+                const float v = element(acc, c);
+                p[(int64_t)c * g.ldo] = round_to<T>(P::kEight ? v * s : v);
+            }
     } else {
-        if (lane_row >= x.na) return;
         T *p = out + (P::kRagged == kContract ? (int64_t)x.e * g.out_expert_stride : 0) +
                (int64_t)(x.a0 + lane_row) * g.ldo + x.b0 + col0;
         const int n = min(C, x.nb - col0);
         const bool per_row = P::kEight && g.w_step_rows == 1;
         const float *s = per_row ? g.w_steps + (int64_t)x.e * g.b_total + x.b0 + col0 : nullptr;
-        constexpr int kVec = 16 / sizeof(T);
-        if (n == C && ((uintptr_t)p & 15) == 0) {
+        auto value = [&](int c) { return per_row ? element(acc, c) * __ldg(s + c) : element(acc, c); };
+        if (n == C && ((uintptr_t)p & 31) == 0) {
+            // one whole 32-byte sector per store
+            constexpr int kVec = 32 / sizeof(T);
 #pragma unroll
             for (int c = 0; c < C; c += kVec) {
-                __align__(16) T v[kVec];
+                uint32_t v[8];
 #pragma unroll
-                for (int u = 0; u < kVec; ++u) v[u] = round_to<T>(per_row ? acc[c + u] * __ldg(s + c + u) : acc[c + u]);
-                *(uint4 *)(p + c) = *(const uint4 *)v;
+                for (int u = 0; u < 8; ++u) {
+                    if constexpr (sizeof(T) == 4) v[u] = __float_as_uint(value(c + u));
+                    else v[u] = word_of<T>(value(c + 2 * u), value(c + 2 * u + 1));
+                }
+                store32(p + c, v);
             }
         } else {
 #pragma unroll
             for (int c = 0; c < C; ++c)
-                if (c < n) p[c] = round_to<T>(per_row ? acc[c] * __ldg(s + c) : acc[c]);
+                if (c < n) p[c] = round_to<T>(value(c));
         }
     }
 }
 
 // Gram tile: entries on and below the diagonal, divided by the group's count,
 // and their mirror images.
-template <int C>
-__device__ __forceinline__ void store_gram(const Args &g, const Tile &x, int lane_row, int col0, const float (&acc)[C])
+template <int N>
+__device__ __forceinline__ void store_gram(const Args &g, const Tile &x, int lane_row, int col0,
+                                           const uint64_t (&acc)[N])
 {
     if (lane_row >= x.na) return;
     const int64_t d = g.ldo;
@@ -214,37 +263,61 @@ __device__ __forceinline__ void store_gram(const Args &g, const Tile &x, int lan
     const int i = x.a0 + lane_row;
     const float count = (float)max(x.count, 1);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
+    for (int c = 0; c < 2 * N; ++c) {
         const int j = x.b0 + col0 + c;
         if (col0 + c < x.nb && j <= i) {
-            const float v = __fdiv_rn(acc[c], count);
+            const float v = __fdiv_rn(element(acc, c), count);
             out[i * d + j] = v;
             out[j * d + i] = v;
         }
     }
 }
 
+// The last stage of a group that ends inside it: rows [valid, 16 steps) of both
+// operands (the next group's, or whatever lies behind the last one) are zeroed
+// in this CTA's shared memory by one warp, NaN and all.
 template <class P>
-__global__ void __launch_bounds__(Shape<P>::kThreads, 1)
+__device__ __forceinline__ void zero_tail(uint8_t *stage, int valid, int steps, int lane)
+{
+    using S = Shape<P>;
+    constexpr int kAtoms = S::kStageBytes / (S::kKB * 128);
+    const int rows = 16 * steps - valid;
+    for (int i = lane; i < kAtoms * rows * 8; i += 32) {
+        const int atom = i / (rows * 8), w = i % (rows * 8);
+        *(uint4 *)(stage + atom * S::kKB * 128 + (valid + (w >> 3)) * 128 + (w & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+
+template <class P>
+__global__ void __cluster_dims__(P::kPair ? 2 : 1, 1, 1) __launch_bounds__(Shape<P>::kThreads, 1)
 mm_kernel(const __grid_constant__ Maps maps, const Args g)
 {
     using S = Shape<P>;
     constexpr int BN = P::kBN;
+    constexpr bool kPair = P::kPair;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint64_t *bars = (uint64_t *)(smem + S::kStages * S::kStageBytes);
-    int *first = (int *)(bars + 32);                        // tile numbering: kMaxExperts + 1
+    int *first = (int *)(bars + 48);                        // tile numbering: kMaxExperts + 1
     float *steps_sh = (float *)(first + kMaxExperts + 4);   // staged row steps (kTokensB, 8-bit)
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = kPair ? (int)cluster_rank() : 0;
     const uint32_t bar0 = smem_u32(bars);
+    // Barriers.  In a pair, full, accumulator-empty and tail-done barriers are
+    // the first CTA's; the others each CTA has for itself.
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (S::kStages + s); };
-    auto accf_bar = [&](int b) { return bar0 + 8u * (2 * S::kStages + b); };
-    auto acce_bar = [&](int b) { return bar0 + 8u * (2 * S::kStages + 2 + b); };
-    const uint32_t drain_bar = bar0 + 8u * (2 * S::kStages + 4);
+    auto tail_full_bar = [&](int s) { return bar0 + 8u * (2 * S::kStages + s); };  // a tail stage has landed in this CTA
+    auto tail_done_bar = [&](int s) { return bar0 + 8u * (3 * S::kStages + s); };  // the CTAs have zeroed their tails
+    auto accf_bar = [&](int b) { return bar0 + 8u * (4 * S::kStages + b); };
+    auto acce_bar = [&](int b) { return bar0 + 8u * (4 * S::kStages + 2 + b); };
+    const uint32_t drain_bar = bar0 + 8u * (4 * S::kStages + 4);
+    static_assert(4 * S::kStages + 5 <= 48, "barriers");
 
     if (threadIdx.x == 0) {
         prefetch_map(&maps.a);
@@ -252,20 +325,29 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
+            mbar_init(tail_full_bar(s), 1);
+            mbar_init(tail_done_bar(s), S::kCtas);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf_bar(b), 1);
-            mbar_init(acce_bar(b), S::kEpiWarps);
+            mbar_init(acce_bar(b), S::kEpiWarps * S::kCtas);
         }
         mbar_init(drain_bar, 1);
         abort_sh = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(&tmem_base_sh)),
-                     "r"(S::kTmemCols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        if (kPair) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(&tmem_base_sh)),
+                         "r"(S::kTmemCols));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(&tmem_base_sh)),
+                         "r"(S::kTmemCols));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
     }
     if (warp == 2) {
         // tile numbering: exclusive prefix sum of the groups' tile counts
@@ -292,9 +374,11 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     }
     tc_fence_before();
     __syncthreads();
+    if (kPair) cluster_sync();  // the other CTA's barriers exist before anything signals them
     tc_fence_after();
     const uint32_t tmem_base = tmem_base_sh;
     const int total = first[g.experts];
+    const int tile0 = blockIdx.x / S::kCtas, tile_step = gridDim.x / S::kCtas;
     volatile int *abort_flag = &abort_sh;
 
     // Bounded wait: false once it has run for the time limit or another role
@@ -314,15 +398,22 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
         }
     };
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < 4) {
+        if constexpr (S::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsOthers));
+        if (warp == 0 && lane == 0) {
             // ---------------- TMA producer
             int it = 0;
+            uint32_t tail_last = 0, tail_count = 0;  // per stage: last use was a tail; parity of its tails
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            for (int t = tile0; t < total && ok; t += tile_step) {
                 const Tile x = find_tile<P>(g, first, t);
                 const int nkb = ceil_div(x.k1 - x.k0, S::kKB);
-                const int boxes = P::kRagged == kTokensB ? ceil_div(x.nb, P::kBoxRows) : 1;
+                const int a0 = x.a0 + rank * kBM;
+                // rows of B this CTA loads: its share of the instruction's N
+                const int share = P::kRagged == kTokensB ? ((x.nb + 15) & ~15) / S::kCtas : S::kBRows;
+                const int b0 = x.b0 + rank * share;
+                const int boxes = P::kRagged == kTokensB ? ceil_div(share, P::kBoxRows) : 1;
+                const uint32_t bytes = P::kRagged == kTokensB ? S::kABytes + boxes * P::kBoxRows * 128 : S::kStageBytes;
                 for (int kb = 0; kb < nkb; ++kb, ++it) {
                     const int s = it % S::kStages;
                     if (it >= S::kStages && !wait(empty_bar(s), (it / S::kStages - 1) & 1, 1000)) {
@@ -331,148 +422,194 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                     }
                     const uint32_t a = smem_u32(smem + s * S::kStageBytes), b = a + P::kPlanes * S::kABytes;
                     const int k = x.k0 + kb * S::kKB;
+                    // In a pair both CTAs' loads complete on the first one's
+                    // barrier.  A tail stage completes on a barrier of its own
+                    // CTA's, whose warp 3 zeroes what lies beyond the group.
+                    const bool tail = P::kRagged == kContract && ((x.k1 - k) & 15) && x.k1 - k < S::kKB;
+                    uint32_t bar = full_bar(s);
+                    tail_last = tail ? tail_last | 1u << s : tail_last & ~(1u << s);
+                    if (tail) {
+                        tail_count ^= 1u << s;
+                        if (!rank) mbar_arrive(bar);  // the stage's phases go on
+                        bar = tail_full_bar(s);
+                        mbar_expect_tx(bar, bytes);
+                        if (kPair) bar = map_rank(bar, rank);
+                    } else if (!kPair) {
+                        mbar_expect_tx(bar, bytes);
+                    } else {
+                        if (!rank) mbar_expect_tx(bar, 2 * bytes);
+                        bar = map_rank(bar, 0);
+                    }
+                    auto load2 = [&](uint32_t dst, const CUtensorMap *m, int cx, int cy) {
+                        if (kPair) tma_load_2d_pair(dst, m, cx, cy, bar);
+                        else tma_load_2d(dst, m, cx, cy, bar);
+                    };
+                    auto load3 = [&](uint32_t dst, const CUtensorMap *m, int cx, int cy, int cz) {
+                        if (kPair) tma_load_3d_pair(dst, m, cx, cy, cz, bar);
+                        else tma_load_3d(dst, m, cx, cy, cz, bar);
+                    };
                     if (P::kRagged == kTokensB) {
-                        mbar_expect_tx(full_bar(s), S::kABytes + boxes * P::kBoxRows * 128);
                         if (P::kAColumns) {
-                            tma_load_3d(a, &maps.a, x.a0, k, x.e, full_bar(s));
-                            tma_load_3d(a + S::kABytes / 2, &maps.a, x.a0 + 64, k, x.e, full_bar(s));
+                            load3(a, &maps.a, a0, k, x.e);
+                            load3(a + S::kABytes / 2, &maps.a, a0 + 64, k, x.e);
                         } else {
-                            tma_load_3d(a, &maps.a, k, x.a0, x.e, full_bar(s));
+                            load3(a, &maps.a, k, a0, x.e);
                         }
                         for (int r = 0; r < boxes; ++r)
-                            tma_load_2d(b + r * P::kBoxRows * 128, &maps.b, k, x.b0 + r * P::kBoxRows, full_bar(s));
+                            load2(b + r * P::kBoxRows * 128, &maps.b, k, b0 + r * P::kBoxRows);
                     } else if (P::kRagged == kTokensA) {
-                        mbar_expect_tx(full_bar(s), S::kStageBytes);
-                        tma_load_2d(a, &maps.a, k, x.a0, full_bar(s));
-                        tma_load_3d(b, &maps.b, k, x.b0, x.e, full_bar(s));
+                        load2(a, &maps.a, k, a0);
+                        load3(b, &maps.b, k, b0, x.e);
                     } else {
-                        mbar_expect_tx(full_bar(s), S::kStageBytes);
 #pragma unroll
                         for (int p = 0; p < P::kPlanes; ++p) {
 #pragma unroll
                             for (int c = 0; c < kBM / 64; ++c)
-                                tma_load_3d(a + p * S::kABytes + c * S::kKB * 128, &maps.a, x.a0 + 64 * c, k, p,
-                                            full_bar(s));
+                                load3(a + p * S::kABytes + c * S::kKB * 128, &maps.a, a0 + 64 * c, k, p);
 #pragma unroll
-                            for (int c = 0; c < BN / 64; ++c)
-                                tma_load_3d(b + p * S::kBBytes + c * S::kKB * 128, &maps.b, x.b0 + 64 * c, k, p,
-                                            full_bar(s));
+                            for (int c = 0; c < S::kBRows / 64; ++c)
+                                load3(b + p * S::kBBytes + c * S::kKB * 128, &maps.b, b0 + 64 * c, k, p);
                         }
                     }
                 }
             }
-            // every issued copy has to land before the CTA may exit
+            // every issued copy has to land before the CTA may exit (in a pair
+            // the first CTA's full barriers count both CTAs' copies)
             for (int i = max(0, it - S::kStages); i < it; ++i) {
+                const int s = i % S::kStages;
+                const bool tail = (tail_last >> s) & 1;
+                if (rank && !tail) continue;
+                const uint32_t bar = tail ? tail_full_bar(s) : full_bar(s);
+                const uint32_t parity = tail ? ((tail_count >> s) & 1) ^ 1 : (i / S::kStages) & 1;
                 const uint64_t t0 = now_ns();
-                while (!mbar_try_wait(full_bar(i % S::kStages), (i / S::kStages) & 1) &&
-                       now_ns() - t0 < g.timeout_ns + 50000000ull) {
+                while (!mbar_try_wait(bar, parity) && now_ns() - t0 < g.timeout_ns + 50000000ull) {
                 }
             }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ---------------- MMA issuer (the whole warp walks the loop; lane 0 issues)
-        int it = 0, chunk = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            const Tile x = find_tile<P>(g, first, t);
-            const int nkb = ceil_div(x.k1 - x.k0, S::kKB);
-            const int n_mma = P::kRagged == kTokensB ? (x.nb + 15) & ~15 : BN;
-            const uint32_t idesc = g.idesc | ((uint32_t)(n_mma >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-            for (int kb = 0; kb < nkb; ++kb, ++it) {
-                const int buf = chunk & 1, in_chunk = kb % P::kChunk;
-                if (in_chunk == 0 && chunk >= 2) ok = wait(acce_bar(buf), ((chunk >> 1) - 1) & 1, 2000);
-                const int s = it % S::kStages;
-                ok = ok && wait(full_bar(s), (it / S::kStages) & 1, 2001);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                uint8_t *stage = smem + s * S::kStageBytes;
-                const uint32_t a = smem_u32(stage), b = a + P::kPlanes * S::kABytes;
-                constexpr int kSteps = S::kKB / (P::kEight ? 32 : 16);
-                int steps = kSteps;
-                if (P::kRagged == kContract) {
-                    // The group may end inside this stage: its last step's
-                    // missing rows (the next group's, or whatever lies behind
-                    // the last one) are zeroed in both operands, NaN and all.
-                    const int valid = min(S::kKB, x.k1 - (x.k0 + kb * S::kKB));
-                    steps = (valid + 15) >> 4;
-                    if (valid & 15) {
-                        constexpr int kAtoms = P::kPlanes * (kBM + BN) / 64;
-                        const int rows = 16 * steps - valid;
-                        for (int i = lane; i < kAtoms * rows * 8; i += 32) {
-                            const int atom = i / (rows * 8), w = i % (rows * 8);
-                            *(uint4 *)(stage + atom * S::kKB * 128 + (valid + (w >> 3)) * 128 + (w & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                    }
+        } else if (warp == 1 && rank == 0 && elect_one()) {
+            // ---------------- MMA issuer
+            int it = 0, chunk = 0;
+            uint32_t tail_parity = 0;  // one bit per stage
+            bool ok = true;
+            // descriptors of stage 0; another address only changes the low bits
+            constexpr bool kACols = P::kRagged == kContract || P::kAColumns, kBCols = P::kRagged == kContract;
+            const uint32_t base = smem_u32(smem), base_b = base + P::kPlanes * S::kABytes;
+            const uint64_t a_desc = kACols ? umma_desc_mn(base, S::kKB * 128) : umma_desc(base);
+            const uint64_t b_desc = kBCols ? umma_desc_mn(base_b, S::kKB * 128) : umma_desc(base_b);
+            constexpr int kSteps = S::kKB / (P::kEight ? 32 : 16);
+            constexpr int kAStep = (kACols ? 2048 : 32) >> 4, kBStep = (kBCols ? 2048 : 32) >> 4;
+            auto mma = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t add) {
+                if (P::kEight) {
+                    if (kPair) umma_f8_pair(d, ad, bd, idesc, add);
+                    else umma_f8(d, ad, bd, idesc, add);
+                } else {
+                    if (kPair) umma_f16_pair(d, ad, bd, idesc, add);
+                    else umma_f16(d, ad, bd, idesc, add);
                 }
-                tc_fence_after();
-                if (lane == 0) {
+            };
+            auto commit = [&](uint32_t bar) {
+                if (kPair) umma_commit_pair(bar);
+                else umma_commit(bar);
+            };
+            for (int t = tile0; t < total && ok; t += tile_step) {
+                const Tile x = find_tile<P>(g, first, t);
+                const int nkb = ceil_div(x.k1 - x.k0, S::kKB);
+                const int n_mma = P::kRagged == kTokensB ? (x.nb + 15) & ~15 : BN;
+                const uint32_t idesc = g.idesc | ((uint32_t)(n_mma >> 3) << 17) | ((uint32_t)(S::kM >> 4) << 24);
+                for (int kb = 0; kb < nkb; ++kb, ++it) {
+                    const int buf = chunk & 1, in_chunk = kb % P::kChunk;
+                    if (in_chunk == 0 && chunk >= 2) ok = wait(acce_bar(buf), ((chunk >> 1) - 1) & 1, 2000);
+                    const int s = it % S::kStages;
+                    ok = ok && wait(full_bar(s), (it / S::kStages) & 1, 2001);
+                    int steps = kSteps;
+                    if (P::kRagged == kContract) {
+                        const int valid = min(S::kKB, x.k1 - (x.k0 + kb * S::kKB));
+                        steps = (valid + 15) >> 4;
+                        if (valid & 15) {
+                            // (the zeroes written there are ordered by an
+                            // acquire at cluster scope once they are complete)
+                            ok = ok && wait(tail_done_bar(s), (tail_parity >> s) & 1, 2002) &&
+                                 mbar_try_wait_cluster(tail_done_bar(s), (tail_parity >> s) & 1);
+                            tail_parity ^= 1u << s;
+                        }
+                    }
+                    if (!ok) break;
+                    tc_fence_after();
                     const uint32_t d = tmem_base + (uint32_t)(buf * S::kAcc * BN);
-                    for (int ks = 0; ks < steps; ++ks) {
-                        const uint32_t fresh = (in_chunk | ks) != 0;
+                    const uint64_t ad = a_desc + (uint32_t)(s * (S::kStageBytes >> 4));
+                    const uint64_t bd = b_desc + (uint32_t)(s * (S::kStageBytes >> 4));
+#pragma unroll
+                    for (int ks = 0; ks < kSteps; ++ks) {
+                        if (P::kRagged == kContract && ks >= steps) break;
+                        const uint32_t add = (in_chunk | ks) != 0;
+                        const uint64_t ak = ad + ks * kAStep, bk = bd + ks * kBStep;
                         if (P::kPlanes > 1) {
                             // x = h + m + l in three bf16 parts: hh into one
                             // accumulator, the five smaller products into another
-                            const uint32_t off = ks * 2048;
-                            uint64_t ad[3], bd[3];
-#pragma unroll
-                            for (int p = 0; p < 3; ++p) {
-                                ad[p] = umma_desc_mn(a + p * S::kABytes + off, S::kKB * 128);
-                                bd[p] = umma_desc_mn(b + p * S::kBBytes + off, S::kKB * 128);
-                            }
-                            umma_f16(d, ad[0], bd[0], idesc, fresh);
-                            umma_f16(d + BN, ad[0], bd[2], idesc, fresh);
-                            umma_f16(d + BN, ad[2], bd[0], idesc, 1);
-                            umma_f16(d + BN, ad[1], bd[1], idesc, 1);
-                            umma_f16(d + BN, ad[0], bd[1], idesc, 1);
-                            umma_f16(d + BN, ad[1], bd[0], idesc, 1);
-                        } else if (P::kRagged == kContract) {
-                            umma_f16(d, umma_desc_mn(a + ks * 2048, S::kKB * 128),
-                                     umma_desc_mn(b + ks * 2048, S::kKB * 128), idesc, fresh);
-                        } else if (P::kEight) {
-                            umma_f8(d, umma_desc(a + ks * 32), umma_desc(b + ks * 32), idesc, fresh);
+                            constexpr uint32_t kAm = S::kABytes >> 4, kBm = S::kBBytes >> 4;
+                            mma(d, ak, bk, idesc, add);
+                            mma(d + BN, ak, bk + 2 * kBm, idesc, add);
+                            mma(d + BN, ak + 2 * kAm, bk, idesc, 1);
+                            mma(d + BN, ak + kAm, bk + kBm, idesc, 1);
+                            mma(d + BN, ak, bk + kBm, idesc, 1);
+                            mma(d + BN, ak + kAm, bk, idesc, 1);
                         } else {
-                            umma_f16(d, P::kAColumns ? umma_desc_mn(a + ks * 2048, S::kKB * 128)
-                                                     : umma_desc(a + ks * 32),
-                                     umma_desc(b + ks * 32), idesc, fresh);
+                            mma(d, ak, bk, idesc, add);
                         }
                     }
-                    umma_commit(empty_bar(s));
-                    if (in_chunk == P::kChunk - 1 || kb == nkb - 1) umma_commit(accf_bar(buf));
+                    commit(empty_bar(s));
+                    if (in_chunk == P::kChunk - 1 || kb == nkb - 1) {
+                        commit(accf_bar(buf));
+                        ++chunk;
+                    }
                 }
-                __syncwarp();
-                if (in_chunk == P::kChunk - 1 || kb == nkb - 1) ++chunk;
             }
-        }
-        if (!ok) {
-            // let issued MMAs finish before TMEM is released
-            if (lane == 0) {
-                umma_commit(drain_bar);
+            if (!ok) {
+                // let issued MMAs finish before TMEM is released
+                commit(drain_bar);
                 const uint64_t t0 = now_ns();
                 while (!mbar_try_wait(drain_bar, 0) && now_ns() - t0 < g.timeout_ns + 50000000ull) {
                 }
             }
-            __syncwarp();
+        } else if (warp == 3 && P::kRagged == kContract) {
+            // ---------------- zero the tails of this CTA's operands
+            int it = 0;
+            uint32_t tail_parity = 0;
+            for (int t = tile0; t < total; t += tile_step) {
+                const Tile x = find_tile<P>(g, first, t);
+                it += ceil_div(x.k1 - x.k0, S::kKB);
+                const int valid = (x.k1 - x.k0) % S::kKB;
+                if (!(valid & 15)) continue;
+                const int s = (it - 1) % S::kStages;
+                if (!__all_sync(0xffffffffu, wait(tail_full_bar(s), (tail_parity >> s) & 1, 2003))) break;
+                tail_parity ^= 1u << s;
+                zero_tail<P>(smem + s * S::kStageBytes, valid, (valid + 15) >> 4, lane);
+                if (lane == 0) {
+                    if (kPair) mbar_arrive_cluster(map_rank(tail_done_bar(s), 0));
+                    else mbar_arrive(tail_done_bar(s));
+                }
+                __syncwarp();
+            }
         }
+        __syncwarp();
     } else {
         // ---------------- epilogue: chunks TMEM -> FP32 registers, then store
+        if constexpr (S::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsEpilogue));
         const int quad = warp & 3;                   // TMEM lanes [32 quad, 32 quad + 32)
-        const int half = (warp - 2) >> 2;            // columns [half kCols, half kCols + kCols)
-        const int lane_row = quad * 32 + lane, col0 = half * S::kCols;
+        const int half = (warp - 4) >> 2;            // columns [half kCols, half kCols + kCols)
+        const int lane_row = rank * kBM + quad * 32 + lane, col0 = half * S::kCols;
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-        float *steps_w = steps_sh + (warp - 2) * 2 * S::kCols;
+        float *steps_w = steps_sh + (warp - 4) * 2 * S::kCols;
         int chunk = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        for (int t = tile0; t < total && ok; t += tile_step) {
             const Tile x = find_tile<P>(g, first, t);
             const int nkb = ceil_div(x.k1 - x.k0, S::kKB);
             const int nchunk = ceil_div(nkb, P::kChunk);
-            float acc[S::kCols];
+            // 32-column loads of each chunk: the tile's valid columns only
+            const int loads = min(max(ceil_div(x.nb - col0, 32), 0), S::kCols / 32) * S::kAcc;
+            uint64_t acc[S::kCols / 2];  // packed pairs of FP32 columns
 #pragma unroll
-            for (int i = 0; i < S::kCols; ++i) acc[i] = 0.f;
+            for (int i = 0; i < S::kCols / 2; ++i) acc[i] = 0;
             // 8-bit operands: the steps of this thread's share of the tile
             const float *xs = nullptr, *ws = nullptr;
             bool own_row = false;
@@ -484,14 +621,17 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                         ws = g.w_steps + ((int64_t)x.e * ceil_div(g.b_total, 128) +
                                           min((x.b0 + col0) / 128, ceil_div(g.b_total, 128) - 1)) * nkb;
                 } else if (g.w_step_rows != 1) {
-                    ws = g.w_steps + ((int64_t)x.e * ceil_div(g.a_total, 128) + x.a0 / 128) * nkb;
+                    ws = g.w_steps + ((int64_t)x.e * ceil_div(g.a_total, 128) +
+                                      min((x.a0 + rank * kBM) / 128, ceil_div(g.a_total, 128) - 1)) * nkb;
                 }
             }
             for (int c = 0; c < nchunk; ++c, ++chunk) {
                 const int buf = chunk & 1;
-                float row_step = 1.f;
-                if (P::kEight && P::kRagged == kTokensA)
-                    row_step = (own_row ? __ldg(xs + c) : 0.f) * (ws ? __ldg(ws + c) : 1.f);
+                uint64_t row_step = 0;
+                if (P::kEight && P::kRagged == kTokensA) {
+                    const float s = (own_row ? __ldg(xs + c) : 0.f) * (ws ? __ldg(ws + c) : 1.f);
+                    row_step = pack2(s, s);
+                }
                 float *steps = steps_w + (c & 1) * S::kCols;
                 if (P::kEight && P::kRagged == kTokensB) {
                     const float s = ws ? __ldg(ws + c) : 1.f;
@@ -503,57 +643,83 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t src = tmem_base + lane_off + (uint32_t)(buf * S::kAcc * BN + col0);
+                auto addr = [&](int l) { return src + (uint32_t)((l / S::kAcc) * 32 + (l % S::kAcc) * BN); };
+                auto add = [&](const uint32_t (&r)[32], int l) {
+                    const int c0 = (l / S::kAcc) * 16;
 #pragma unroll
-                for (int c0 = 0; c0 < S::kCols; c0 += 32) {
-                    if (col0 + c0 < x.nb) {
-                        float v[32];
-                        tmem_ld32(src + c0, v);
-                        if (P::kEight && P::kRagged == kTokensA) {
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t v = pack2(r[2 * i], r[2 * i + 1]);
+                        if (P::kEight && P::kRagged == kTokensA) fma2(acc[c0 + i], v, row_step);
+                        else if (P::kEight) fma2(acc[c0 + i], v, *(const uint64_t *)(steps + 2 * (c0 + i)));
+                        else add2(acc[c0 + i], v);
+                    }
+                };
+                // one load in flight while the one before it is added
+                uint32_t ra[32], rb[32];
+                constexpr int kLoads = S::kCols / 32 * S::kAcc;
+                if (loads > 0) tmem_ld32_start(addr(0), ra);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) acc[c0 + i] = fmaf(v[i], row_step, acc[c0 + i]);
-                        } else if (P::kEight) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) acc[c0 + i] = fmaf(v[i], steps[c0 + i], acc[c0 + i]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) acc[c0 + i] += v[i];
-                        }
-                        if (P::kPlanes > 1) {
-                            tmem_ld32(src + BN + c0, v);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) acc[c0 + i] += v[i];
-                        }
+                for (int l = 0; l < kLoads; l += 2) {
+                    if (l < loads) {
+                        tmem_ld32_wait(ra);
+                        if (l + 1 < kLoads && l + 1 < loads) tmem_ld32_start(addr(l + 1), rb);
+                        add(ra, l);
+                    }
+                    if (l + 1 < kLoads && l + 1 < loads) {
+                        tmem_ld32_wait(rb);
+                        if (l + 2 < kLoads && l + 2 < loads) tmem_ld32_start(addr(l + 2), ra);
+                        add(rb, l + 1);
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(acce_bar(buf));
+                if (lane == 0) {
+                    if (kPair) mbar_arrive_remote(map_rank(acce_bar(buf), 0));
+                    else mbar_arrive(acce_bar(buf));
+                }
             }
             if (!ok) break;
-            if (P::kLower) store_gram<S::kCols>(g, x, lane_row, col0, acc);
-            else if (g.out_type == BAKRON_BF16) store_tile<P, __nv_bfloat16, S::kCols>(g, x, lane_row, col0, acc);
-            else if (g.out_type == BAKRON_F16) store_tile<P, __half, S::kCols>(g, x, lane_row, col0, acc);
-            else store_tile<P, float, S::kCols>(g, x, lane_row, col0, acc);
+            if constexpr (P::kLower) store_gram(g, x, lane_row, col0, acc);
+            else if (g.out_type == BAKRON_BF16) store_tile<P, __nv_bfloat16>(g, x, lane_row, col0, acc);
+            else if (g.out_type == BAKRON_F16) store_tile<P, __half>(g, x, lane_row, col0, acc);
+            else store_tile<P, float>(g, x, lane_row, col0, acc);
         }
     }
     tc_fence_before();
     __syncthreads();
+    if (kPair) cluster_sync();  // neither CTA leaves while the other can still reach its memory
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(S::kTmemCols));
+        if (kPair)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(S::kTmemCols));
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(S::kTmemCols));
     }
 }
 
 template <class P>
 cudaError_t configure()
 {
-    return cudaFuncSetAttribute(mm_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<P>::kSmem);
+    using S = Shape<P>;
+    if (S::kSplitRegs) {
+        // refuse a build whose launch does not bring the registers the
+        // warpgroups will ask for: they would wait for them for ever
+        cudaFuncAttributes a;
+        const cudaError_t e = cudaFuncGetAttributes(&a, mm_kernel<P>);
+        if (e != cudaSuccess) return e;
+        if (a.numRegs * S::kThreads < S::kRegsNeeded) return cudaErrorLaunchOutOfResources;
+    }
+    return cudaFuncSetAttribute(mm_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
 }
 
+// As many CTAs as the device has SMs (`sms`), fewer if there are fewer tiles
+// (`tiles`, an upper bound).
 template <class P>
-cudaError_t launch(const Maps &maps, const Args &g, int blocks, cudaStream_t stream)
+cudaError_t launch(const Maps &maps, const Args &g, int64_t tiles, int sms, cudaStream_t stream)
 {
-    mm_kernel<P><<<blocks, Shape<P>::kThreads, Shape<P>::kSmem, stream>>>(maps, g);
+    using S = Shape<P>;
+    const int64_t groups = min64(tiles, sms / S::kCtas);
+    mm_kernel<P><<<(unsigned)(groups * S::kCtas), S::kThreads, S::kSmem, stream>>>(maps, g);
     return cudaGetLastError();
 }
 

@@ -15,14 +15,14 @@ namespace mm {
 namespace {
 struct Outer {
     static constexpr Ragged kRagged = kContract;
-    static constexpr bool kEight = false, kAColumns = true, kLower = false;
+    static constexpr bool kPair = true, kEight = false, kAColumns = true, kLower = false;
     static constexpr int kBN = 256, kPlanes = 1, kChunk = 4, kKRows = 64, kBoxRows = 64;
 };
 template <int Planes>
 struct Gram {
     static constexpr Ragged kRagged = kContract;
-    static constexpr bool kEight = false, kAColumns = true, kLower = true;
-    static constexpr int kBN = 128, kPlanes = Planes, kChunk = 4, kKRows = Planes > 1 ? 32 : 64, kBoxRows = kKRows;
+    static constexpr bool kPair = true, kEight = false, kAColumns = true, kLower = true;
+    static constexpr int kBN = Planes > 1 ? 128 : 256, kPlanes = Planes, kChunk = 4, kKRows = Planes > 1 ? 32 : 64, kBoxRows = kKRows;
 };
 
 // Three bf16 parts of an fp32 matrix, each rounded to nearest from what the
@@ -82,12 +82,13 @@ cudaError_t configure_outer()
     return e == cudaSuccess ? configure<Gram<3>>() : e;
 }
 
-cudaError_t launch_outer(Variant v, const Maps &maps, const Args &g, int blocks, cudaStream_t stream)
+cudaError_t launch_outer(Variant v, const Maps &maps, const Args &g, int64_t tiles, int sms,
+                        cudaStream_t stream)
 {
     switch (v) {
-    case kOuter: return launch<Outer>(maps, g, blocks, stream);
-    case kGramOne: return launch<Gram<1>>(maps, g, blocks, stream);
-    default: return launch<Gram<3>>(maps, g, blocks, stream);
+    case kOuter: return launch<Outer>(maps, g, tiles, sms, stream);
+    case kGramOne: return launch<Gram<1>>(maps, g, tiles, sms, stream);
+    default: return launch<Gram<3>>(maps, g, tiles, sms, stream);
     }
 }
 

@@ -11,7 +11,7 @@ namespace {
 template <int BN, bool AColumns>
 struct Rows {
     static constexpr Ragged kRagged = kTokensB;
-    static constexpr bool kEight = false, kAColumns = AColumns, kLower = false;
+    static constexpr bool kPair = BN == 256, kEight = false, kAColumns = AColumns, kLower = false;
     static constexpr int kBN = BN, kPlanes = 1, kChunk = 4, kKRows = 0;
     static constexpr int kBoxRows = BN == 256 ? 64 : 32;
 };
@@ -26,13 +26,14 @@ cudaError_t configure_rows()
     return e;
 }
 
-cudaError_t launch_rows(Variant v, const Maps &maps, const Args &g, int blocks, cudaStream_t stream)
+cudaError_t launch_rows(Variant v, const Maps &maps, const Args &g, int64_t tiles, int sms,
+                        cudaStream_t stream)
 {
     switch (v) {
-    case kRows256: return launch<Rows<256, false>>(maps, g, blocks, stream);
-    case kRows64: return launch<Rows<64, false>>(maps, g, blocks, stream);
-    case kRowsDx256: return launch<Rows<256, true>>(maps, g, blocks, stream);
-    default: return launch<Rows<64, true>>(maps, g, blocks, stream);
+    case kRows256: return launch<Rows<256, false>>(maps, g, tiles, sms, stream);
+    case kRows64: return launch<Rows<64, false>>(maps, g, tiles, sms, stream);
+    case kRowsDx256: return launch<Rows<256, true>>(maps, g, tiles, sms, stream);
+    default: return launch<Rows<64, true>>(maps, g, tiles, sms, stream);
     }
 }
 
