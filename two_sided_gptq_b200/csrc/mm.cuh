@@ -15,6 +15,7 @@ constexpr int kMaxExperts = 1024;
 
 struct Maps {
     CUtensorMap a, b;
+    CUtensorMap b2;  // packed rows on D's columns: boxes of twice as many rows
 };
 
 struct Args {
@@ -25,6 +26,7 @@ struct Args {
     void *out;
     int64_t ldo, out_expert_stride;  // elements
     int out_type;                    // bakron_type_t
+    int turn;                        // 16-bit result whose rows all start on 16-byte boundaries
     uint32_t idesc;                  // MMA instruction descriptor without M and N
     const float *x_steps, *w_steps;  // 8-bit operands' steps
     int w_step_rows;                 // rows per weight step: 128, or 1 (one step per row)

@@ -148,11 +148,13 @@ bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t 
     g.out = y;
     g.ldo = ldy;
     g.out_type = y_type;
+    g.turn = y_type != BAKRON_F32 && ldy % 8 == 0;
     g.idesc = idesc16(type, columns, false);
     Maps m;
     const CUtensorMapDataType t = map_type(type);
     if (!map3(&m.a, t, 2, w, k, n, ldw, experts, w_stride, 64, columns ? 64 : 128) ||
-        !map2(&m.b, t, 2, x, in, rows, ldx, 64, small ? 32 : 64))
+        !map2(&m.b, t, 2, x, in, rows, ldx, 64, small ? 32 : 64) ||
+        !map2(&m.b2, t, 2, x, in, rows, ldx, 64, small ? 64 : 128))
         return BAKRON_ERR_CUDA;
     const Variant v = columns ? (small ? kRowsDx64 : kRowsDx256) : (small ? kRows64 : kRows256);
     if (launch_rows(v, m, g, tiles, sms, (cudaStream_t)stream) != cudaSuccess) return BAKRON_ERR_CUDA;
@@ -247,7 +249,8 @@ bakron_status_t bakron_matmul_blocks(const uint8_t *x_dev, int64_t x_row_stride,
     const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     CUtensorMap *xm = small ? &m.b : &m.a, *wm = small ? &m.a : &m.b;
     if (!map2(xm, t, 1, x_dev, k, rows, x_row_stride, 128, small ? 32 : 128) ||
-        !map3(wm, t, 1, w_dev, k, n, w_row_stride, experts, w_expert_stride, 128, 128))
+        (small && !map2(&m.b2, t, 1, x_dev, k, rows, x_row_stride, 128, 64)) ||
+        !map3(wm, t, 1, w_dev, k, n, w_row_stride, experts, w_expert_stride, 128, small ? 128 : 64))
         return BAKRON_ERR_CUDA;
     if (launch_eight(small ? kEightB64 : kEightA256, m, g, tiles, sms, (cudaStream_t)stream) !=
         cudaSuccess)
@@ -380,6 +383,7 @@ bakron_status_t bakron_gram_grouped(const void *X_dev, int32_t type, int64_t x_r
             return BAKRON_ERR_CUDA;
     }
     m.b = m.a;
+    m.b2 = m.a;
     if (launch_outer(type == BAKRON_F32 ? kGramThree : kGramOne, m, g, tiles, sms, st) != cudaSuccess)
         return BAKRON_ERR_CUDA;
     return launch_gram_damp(A_dev, d, (int)experts, damping, g.st, st) == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA;

@@ -48,7 +48,7 @@ namespace mm {
 using namespace tc;
 
 constexpr int kBM = 128;
-constexpr int kReserve = 9 * 1024;  // barriers, tile numbering, alignment, staged steps
+constexpr int kReserve = 10 * 1024;  // barriers, tile numbering, alignment, staged steps
 
 template <class P>
 struct Shape {
@@ -61,19 +61,29 @@ struct Shape {
     static constexpr int kABytes = P::kRagged == kContract ? kBM / 64 * kKB * 128 : kBM * 128;
     static constexpr int kBBytes = P::kRagged == kContract ? kBRows / 64 * kKB * 128 : kBRows * 128;
     static constexpr int kStageBytes = P::kPlanes * (kABytes + kBBytes);
-    static constexpr int kStages = (227 * 1024 - kReserve) / kStageBytes < 8 ? (227 * 1024 - kReserve) / kStageBytes : 8;
+    // shared memory in which results are turned (store_turned)
+    static constexpr bool kTurn = P::kRagged == kTokensB && P::kBN == 256;
+    static constexpr int kTurnSpace = kTurn ? 2 * 32 * kBM * 2 : 0;
+    static constexpr int kEpiWarps = 8;
+    static constexpr int kCols = P::kBN / (kEpiWarps / 4);          // columns per epilogue thread
+    // a warp's staged steps: two chunks of its columns' (kTokensB), or one of them
+    static constexpr int kStepFloats = P::kRagged == kTokensB ? 2 * kCols : kCols;
+    static constexpr int kRing = 227 * 1024 - kReserve - kTurnSpace;
+    static constexpr int kStages = kRing / kStageBytes < 8 ? kRing / kStageBytes : 8;
     static constexpr int kAcc = P::kPlanes > 1 ? 2 : 1;             // accumulators per buffer
     static constexpr int kTmemCols = 2 * kAcc * P::kBN;
-    static constexpr int kEpiWarps = 8;
+    // 8-bit chunks are short (one stage): the tile's two column halves are
+    // separate MMAs with separate barriers, so that each is read out while the
+    // other is computed
+    static constexpr int kHalves = P::kEight && P::kRagged == kTokensA ? 2 : 1;
     static constexpr int kThreads = 128 + 32 * kEpiWarps;
-    static constexpr int kCols = P::kBN / (kEpiWarps / 4);          // columns per epilogue thread
     // registers: the epilogue's accumulators and two loads in flight need more
     // than a 12-warp CTA's even share (168), the other warps far less
     static constexpr bool kSplitRegs = kCols > 64;
     static constexpr int kRegsOthers = 56, kRegsEpilogue = 224;
     // a warpgroup can only take registers that the block was launched with
     static constexpr int kRegsNeeded = 128 * kRegsOthers + 32 * kEpiWarps * kRegsEpilogue;
-    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kReserve;
+    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kTurnSpace + kReserve;
 };
 
 // One output tile: group e, D rows a0.. (na valid), D columns b0.. (nb valid),
@@ -227,9 +237,7 @@ __device__ __forceinline__ void store_tile(const Args &g, const Tile &x, int lan
         T *p = out + (P::kRagged == kContract ? (int64_t)x.e * g.out_expert_stride : 0) +
                (int64_t)(x.a0 + lane_row) * g.ldo + x.b0 + col0;
         const int n = min(C, x.nb - col0);
-        const bool per_row = P::kEight && g.w_step_rows == 1;
-        const float *s = per_row ? g.w_steps + (int64_t)x.e * g.b_total + x.b0 + col0 : nullptr;
-        auto value = [&](int c) { return per_row ? element(acc, c) * __ldg(s + c) : element(acc, c); };
+        auto value = [&](int c) { return element(acc, c); };
         if (n == C && ((uintptr_t)p & 31) == 0) {
             // one whole 32-byte sector per store
             constexpr int kVec = 32 / sizeof(T);
@@ -251,6 +259,53 @@ __device__ __forceinline__ void store_tile(const Args &g, const Tile &x, int lan
     }
 }
 
+// kTokensB, 16-bit results whose rows keep 16-byte alignment: the four warps of
+// a column half turn 32 packed rows at a time in shared memory and write whole
+// 256-byte row pieces.  (Written from the accumulators' own lanes, a warp's
+// store is 64 bytes: 128 of them per thread held the next tile's MMAs up.)
+constexpr int kTurnRows = 32;
+constexpr int kTurnBytes = kTurnRows * kBM * 2;
+template <class P, typename T, int N>
+__device__ __forceinline__ void store_turned(const Args &g, const Tile &x, int rank, int thread, int half,
+                                             const uint64_t (&acc)[N], T *buf)
+{
+    const int row0 = rank * kBM;                 // this CTA's first D row
+    const int col0 = half * 2 * N;
+    float s = 1.f;
+    if (P::kEight && g.w_step_rows == 1 && row0 + thread < x.na)
+        s = __ldg(g.w_steps + (int64_t)x.e * g.a_total + x.a0 + row0 + thread);
+    const int piece = (thread & 15) * 8;         // D rows this thread writes: 8 of the CTA's 128
+    const int valid = x.na - row0 - piece;
+    T *out = (T *)g.out + (int64_t)(x.b0 + col0) * g.ldo + x.a0 + row0 + piece;
+#pragma unroll
+    for (int c0 = 0; c0 < 2 * N; c0 += kTurnRows) {
+        if (col0 + c0 >= x.nb) break;
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+#pragma unroll
+        for (int c = 0; c < kTurnRows; ++c) {
+            const float v = element(acc, c0 + c);
+            buf[c * kBM + thread] = round_to<T>(P::kEight ? v * s : v);
+        }
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+#pragma unroll
+        for (int r = 0; r < kTurnRows; r += 8) {
+            const int t = r + (thread >> 4);
+            if (col0 + c0 + t < x.nb) {
+                const uint4 v = *(const uint4 *)(buf + t * kBM + piece);
+                T *p = out + (int64_t)(c0 + t) * g.ldo;
+                if (valid >= 8) {
+                    *(uint4 *)p = v;
+                } else {
+                    const T *e = (const T *)&v;
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (u < valid) p[u] = e[u];
+                }
+            }
+        }
+    }
+}
+
 // Gram tile: entries on and below the diagonal, divided by the group's count,
 // and their mirror images.
 template <int N>
@@ -260,15 +315,31 @@ __device__ __forceinline__ void store_gram(const Args &g, const Tile &x, int lan
     if (lane_row >= x.na) return;
     const int64_t d = g.ldo;
     float *out = (float *)g.out + (int64_t)x.e * g.out_expert_stride;
-    const int i = x.a0 + lane_row;
-    const float count = (float)max(x.count, 1);
+    const int i = x.a0 + lane_row, j0 = x.b0 + col0;
+    const float count = (float)max(x.count, 1), rcount = __frcp_rn(count);
+    auto value = [&](int c) { return div_rn_recip(element(acc, c), count, rcount); };
+    float *row = out + i * d + j0, *col = out + j0 * d + i;
+    if (j0 + 2 * N <= x.a0 && ((uintptr_t)row & 31) == 0) {
+        // below the diagonal throughout: whole 32-byte sectors along the row,
+        // and a warp's 32 rows next to each other in the mirror image
+#pragma unroll
+        for (int c = 0; c < 2 * N; c += 8) {
+            uint32_t v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                v[u] = __float_as_uint(value(c + u));
+                col[(int64_t)(c + u) * d] = __uint_as_float(v[u]);
+            }
+            store32(row + c, v);
+        }
+        return;
+    }
 #pragma unroll
     for (int c = 0; c < 2 * N; ++c) {
-        const int j = x.b0 + col0 + c;
-        if (col0 + c < x.nb && j <= i) {
-            const float v = __fdiv_rn(element(acc, c), count);
-            out[i * d + j] = v;
-            out[j * d + i] = v;
+        if (col0 + c < x.nb && j0 + c <= i) {
+            const float v = value(c);
+            row[c] = v;
+            col[(int64_t)c * d] = v;
         }
     }
 }
@@ -299,7 +370,8 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     constexpr bool kPair = P::kPair;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint64_t *bars = (uint64_t *)(smem + S::kStages * S::kStageBytes);
+    uint8_t *turn_sh = smem + S::kStages * S::kStageBytes;
+    uint64_t *bars = (uint64_t *)(turn_sh + S::kTurnSpace);
     int *first = (int *)(bars + 48);                        // tile numbering: kMaxExperts + 1
     float *steps_sh = (float *)(first + kMaxExperts + 4);   // staged row steps (kTokensB, 8-bit)
     __shared__ uint32_t tmem_base_sh;
@@ -314,10 +386,10 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     auto empty_bar = [&](int s) { return bar0 + 8u * (S::kStages + s); };
     auto tail_full_bar = [&](int s) { return bar0 + 8u * (2 * S::kStages + s); };  // a tail stage has landed in this CTA
     auto tail_done_bar = [&](int s) { return bar0 + 8u * (3 * S::kStages + s); };  // the CTAs have zeroed their tails
-    auto accf_bar = [&](int b) { return bar0 + 8u * (4 * S::kStages + b); };
-    auto acce_bar = [&](int b) { return bar0 + 8u * (4 * S::kStages + 2 + b); };
-    const uint32_t drain_bar = bar0 + 8u * (4 * S::kStages + 4);
-    static_assert(4 * S::kStages + 5 <= 48, "barriers");
+    auto accf_bar = [&](int b, int h) { return bar0 + 8u * (4 * S::kStages + 2 * h + b); };
+    auto acce_bar = [&](int b, int h) { return bar0 + 8u * (4 * S::kStages + 4 + 2 * h + b); };
+    const uint32_t drain_bar = bar0 + 8u * (4 * S::kStages + 8);
+    static_assert(4 * S::kStages + 9 <= 48, "barriers");
 
     if (threadIdx.x == 0) {
         prefetch_map(&maps.a);
@@ -328,10 +400,11 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             mbar_init(tail_full_bar(s), 1);
             mbar_init(tail_done_bar(s), S::kCtas);
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(accf_bar(b), 1);
-            mbar_init(acce_bar(b), S::kEpiWarps * S::kCtas);
-        }
+        for (int b = 0; b < 2; ++b)
+            for (int h = 0; h < S::kHalves; ++h) {
+                mbar_init(accf_bar(b, h), 1);
+                mbar_init(acce_bar(b, h), S::kEpiWarps * S::kCtas / S::kHalves);
+            }
         mbar_init(drain_bar, 1);
         abort_sh = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -400,8 +473,9 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
 
     if (warp < 4) {
         if constexpr (S::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsOthers));
-        if (warp == 0 && lane == 0) {
+        if (warp == 0 && elect_one()) {
             // ---------------- TMA producer
+            const uint32_t first_cta = kPair ? map_rank(bar0, 0) : bar0;  // the pair's first CTA's barriers
             int it = 0;
             uint32_t tail_last = 0, tail_count = 0;  // per stage: last use was a tail; parity of its tails
             bool ok = true;
@@ -438,7 +512,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                         mbar_expect_tx(bar, bytes);
                     } else {
                         if (!rank) mbar_expect_tx(bar, 2 * bytes);
-                        bar = map_rank(bar, 0);
+                        bar = first_cta + 8u * s;
                     }
                     auto load2 = [&](uint32_t dst, const CUtensorMap *m, int cx, int cy) {
                         if (kPair) tma_load_2d_pair(dst, m, cx, cy, bar);
@@ -455,11 +529,18 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                         } else {
                             load3(a, &maps.a, k, a0, x.e);
                         }
-                        for (int r = 0; r < boxes; ++r)
-                            load2(b + r * P::kBoxRows * 128, &maps.b, k, b0 + r * P::kBoxRows);
+                        if (boxes == 2) {
+                            load2(b, &maps.b2, k, b0);
+                        } else {
+                            for (int r = 0; r < boxes; ++r)
+                                load2(b + r * P::kBoxRows * 128, &maps.b, k, b0 + r * P::kBoxRows);
+                        }
                     } else if (P::kRagged == kTokensA) {
                         load2(a, &maps.a, k, a0);
-                        load3(b, &maps.b, k, b0, x.e);
+#pragma unroll
+                        for (int h = 0; h < S::kHalves; ++h)
+                            load3(b + h * S::kBBytes / S::kHalves, &maps.b, k,
+                                  x.b0 + (h * S::kCtas + rank) * (S::kBRows / S::kHalves), x.e);
                     } else {
 #pragma unroll
                         for (int p = 0; p < P::kPlanes; ++p) {
@@ -513,12 +594,13 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             for (int t = tile0; t < total && ok; t += tile_step) {
                 const Tile x = find_tile<P>(g, first, t);
                 const int nkb = ceil_div(x.k1 - x.k0, S::kKB);
-                const int n_mma = P::kRagged == kTokensB ? (x.nb + 15) & ~15 : BN;
+                const int n_mma = P::kRagged == kTokensB ? (x.nb + 15) & ~15 : BN / S::kHalves;
                 const uint32_t idesc = g.idesc | ((uint32_t)(n_mma >> 3) << 17) | ((uint32_t)(S::kM >> 4) << 24);
                 for (int kb = 0; kb < nkb; ++kb, ++it) {
                     const int buf = chunk & 1, in_chunk = kb % P::kChunk;
-                    if (in_chunk == 0 && chunk >= 2) ok = wait(acce_bar(buf), ((chunk >> 1) - 1) & 1, 2000);
                     const int s = it % S::kStages;
+                    if (S::kHalves == 1 && in_chunk == 0 && chunk >= 2)
+                        ok = wait(acce_bar(buf, 0), ((chunk >> 1) - 1) & 1, 2000);
                     ok = ok && wait(full_bar(s), (it / S::kStages) & 1, 2001);
                     int steps = kSteps;
                     if (P::kRagged == kContract) {
@@ -537,29 +619,46 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                     const uint32_t d = tmem_base + (uint32_t)(buf * S::kAcc * BN);
                     const uint64_t ad = a_desc + (uint32_t)(s * (S::kStageBytes >> 4));
                     const uint64_t bd = b_desc + (uint32_t)(s * (S::kStageBytes >> 4));
+                    if constexpr (S::kHalves > 1) {
 #pragma unroll
-                    for (int ks = 0; ks < kSteps; ++ks) {
-                        if (P::kRagged == kContract && ks >= steps) break;
-                        const uint32_t add = (in_chunk | ks) != 0;
-                        const uint64_t ak = ad + ks * kAStep, bk = bd + ks * kBStep;
-                        if (P::kPlanes > 1) {
-                            // x = h + m + l in three bf16 parts: hh into one
-                            // accumulator, the five smaller products into another
-                            constexpr uint32_t kAm = S::kABytes >> 4, kBm = S::kBBytes >> 4;
-                            mma(d, ak, bk, idesc, add);
-                            mma(d + BN, ak, bk + 2 * kBm, idesc, add);
-                            mma(d + BN, ak + 2 * kAm, bk, idesc, 1);
-                            mma(d + BN, ak + kAm, bk + kBm, idesc, 1);
-                            mma(d + BN, ak, bk + kBm, idesc, 1);
-                            mma(d + BN, ak + kAm, bk, idesc, 1);
-                        } else {
-                            mma(d, ak, bk, idesc, add);
+                        for (int h = 0; h < S::kHalves; ++h) {
+                            ok = ok && (chunk < 2 || wait(acce_bar(buf, h), ((chunk >> 1) - 1) & 1, 2000));
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int ks = 0; ks < kSteps; ++ks)
+                                mma(d + h * (BN / S::kHalves), ad + ks * kAStep,
+                                    bd + ks * kBStep + h * (S::kBBytes / S::kHalves >> 4), idesc, ks != 0);
+                            commit(accf_bar(buf, h));
                         }
-                    }
-                    commit(empty_bar(s));
-                    if (in_chunk == P::kChunk - 1 || kb == nkb - 1) {
-                        commit(accf_bar(buf));
+                        if (!ok) break;
+                        commit(empty_bar(s));
                         ++chunk;
+                    } else {
+#pragma unroll
+                        for (int ks = 0; ks < kSteps; ++ks) {
+                            if (P::kRagged == kContract && ks >= steps) break;
+                            const uint32_t add = (in_chunk | ks) != 0;
+                            const uint64_t ak = ad + ks * kAStep, bk = bd + ks * kBStep;
+                            if (P::kPlanes > 1) {
+                                // x = h + m + l in three bf16 parts: hh into one
+                                // accumulator, the five smaller products into another
+                                constexpr uint32_t kAm = S::kABytes >> 4, kBm = S::kBBytes >> 4;
+                                mma(d, ak, bk, idesc, add);
+                                mma(d + BN, ak, bk + 2 * kBm, idesc, add);
+                                mma(d + BN, ak + 2 * kAm, bk, idesc, 1);
+                                mma(d + BN, ak + kAm, bk + kBm, idesc, 1);
+                                mma(d + BN, ak, bk + kBm, idesc, 1);
+                                mma(d + BN, ak + kAm, bk, idesc, 1);
+                            } else {
+                                mma(d, ak, bk, idesc, add);
+                            }
+                        }
+                        commit(empty_bar(s));
+                        if (in_chunk == P::kChunk - 1 || kb == nkb - 1) {
+                            commit(accf_bar(buf, 0));
+                            ++chunk;
+                        }
                     }
                 }
             }
@@ -598,15 +697,16 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
         const int half = (warp - 4) >> 2;            // columns [half kCols, half kCols + kCols)
         const int lane_row = rank * kBM + quad * 32 + lane, col0 = half * S::kCols;
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-        float *steps_w = steps_sh + (warp - 4) * 2 * S::kCols;
+        float *steps_w = steps_sh + (warp - 4) * S::kStepFloats;
+        const uint32_t first_cta_acce = kPair ? map_rank(acce_bar(0, 0), 0) : acce_bar(0, 0);
         int chunk = 0;
         bool ok = true;
         for (int t = tile0; t < total && ok; t += tile_step) {
             const Tile x = find_tile<P>(g, first, t);
             const int nkb = ceil_div(x.k1 - x.k0, S::kKB);
             const int nchunk = ceil_div(nkb, P::kChunk);
-            // 32-column loads of each chunk: the tile's valid columns only
-            const int loads = min(max(ceil_div(x.nb - col0, 32), 0), S::kCols / 32) * S::kAcc;
+            // 16-column loads of each chunk: the tile's valid columns only
+            const int loads = min(max(ceil_div(x.nb - col0, 16), 0), S::kCols / 16) * S::kAcc;
             uint64_t acc[S::kCols / 2];  // packed pairs of FP32 columns
 #pragma unroll
             for (int i = 0; i < S::kCols / 2; ++i) acc[i] = 0;
@@ -625,12 +725,32 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                                       min((x.a0 + rank * kBM) / 128, ceil_div(g.a_total, 128) - 1)) * nkb;
                 }
             }
+            // (kTokensA: the row's steps are fetched four chunks at a time, the
+            // weight's one, a chunk or more ahead of their use)
+            float4 xs_now = make_float4(0, 0, 0, 0), xs_next = xs_now;
+            float ws_next = ws ? __ldg(ws) : 1.f;
+            const bool xs_vec = (nkb & 3) == 0;  // the row's steps start on a 16-byte boundary
+            auto four_steps = [&](int c) {
+                if (xs_vec) return __ldg((const float4 *)(xs + c));
+                return make_float4(__ldg(xs + c), c + 1 < nkb ? __ldg(xs + c + 1) : 0.f,
+                                   c + 2 < nkb ? __ldg(xs + c + 2) : 0.f, c + 3 < nkb ? __ldg(xs + c + 3) : 0.f);
+            };
+            if (own_row) xs_next = four_steps(0);
+            const int bar_half = S::kHalves > 1 ? half : 0;
             for (int c = 0; c < nchunk; ++c, ++chunk) {
                 const int buf = chunk & 1;
                 uint64_t row_step = 0;
                 if (P::kEight && P::kRagged == kTokensA) {
-                    const float s = (own_row ? __ldg(xs + c) : 0.f) * (ws ? __ldg(ws + c) : 1.f);
+                    if ((c & 3) == 0) {
+                        xs_now = xs_next;
+                        if (own_row && c + 4 < nchunk) xs_next = four_steps(c + 4);
+                    }
+                    const float s = xs_now.x * ws_next;
                     row_step = pack2(s, s);
+                    xs_now.x = xs_now.y;
+                    xs_now.y = xs_now.z;
+                    xs_now.z = xs_now.w;
+                    if (ws && c + 1 < nchunk) ws_next = __ldg(ws + c + 1);
                 }
                 float *steps = steps_w + (c & 1) * S::kCols;
                 if (P::kEight && P::kRagged == kTokensB) {
@@ -639,48 +759,82 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                         steps[j] = col0 + j < x.nb ? __ldg(g.x_steps + (int64_t)(x.b0 + col0 + j) * nkb + c) * s : 0.f;
                     __syncwarp();
                 }
-                ok = __all_sync(0xffffffffu, wait(accf_bar(buf), (chunk >> 1) & 1, 3000));
+                ok = __all_sync(0xffffffffu, wait(accf_bar(buf, bar_half), (chunk >> 1) & 1, 3000));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t src = tmem_base + lane_off + (uint32_t)(buf * S::kAcc * BN + col0);
-                auto addr = [&](int l) { return src + (uint32_t)((l / S::kAcc) * 32 + (l % S::kAcc) * BN); };
-                auto add = [&](const uint32_t (&r)[32], int l) {
-                    const int c0 = (l / S::kAcc) * 16;
+                auto addr = [&](int l) { return src + (uint32_t)((l / S::kAcc) * 16 + (l % S::kAcc) * BN); };
+                auto add = [&](const uint32_t (&r)[16], int l) {
+                    const int c0 = (l / S::kAcc) * 8;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < 8; ++i) {
                         const uint64_t v = pack2(r[2 * i], r[2 * i + 1]);
                         if (P::kEight && P::kRagged == kTokensA) fma2(acc[c0 + i], v, row_step);
                         else if (P::kEight) fma2(acc[c0 + i], v, *(const uint64_t *)(steps + 2 * (c0 + i)));
                         else add2(acc[c0 + i], v);
                     }
                 };
-                // one load in flight while the one before it is added
-                uint32_t ra[32], rb[32];
-                constexpr int kLoads = S::kCols / 32 * S::kAcc;
-                if (loads > 0) tmem_ld32_start(addr(0), ra);
+                constexpr int kLoads = S::kCols / 16 * S::kAcc;
+                // the buffer is free once its last load has arrived
+                auto release = [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        const uint32_t bar = first_cta_acce + 8u * (2 * bar_half + buf);
+                        if (kPair) mbar_arrive_remote(bar);
+                        else mbar_arrive(bar);
+                    }
+                };
+                if (loads == kLoads) {
+                    // one load in flight while the one before it is added
+                    // (straight-line code: the loads' registers then feed the
+                    // additions without copies)
+                    uint32_t r[kLoads][16];
+                    tmem_ld16_start(addr(0), r[0]);
 #pragma unroll
-                for (int l = 0; l < kLoads; l += 2) {
-                    if (l < loads) {
-                        tmem_ld32_wait(ra);
-                        if (l + 1 < kLoads && l + 1 < loads) tmem_ld32_start(addr(l + 1), rb);
-                        add(ra, l);
+                    for (int l = 0; l < kLoads; ++l) {
+                        tmem_ld16_wait(r[l]);
+                        if (l + 1 < kLoads) tmem_ld16_start(addr(l + 1), r[l + 1]);
+                        else release();
+                        add(r[l], l);
                     }
-                    if (l + 1 < kLoads && l + 1 < loads) {
-                        tmem_ld32_wait(rb);
-                        if (l + 2 < kLoads && l + 2 < loads) tmem_ld32_start(addr(l + 2), ra);
-                        add(rb, l + 1);
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (kPair) mbar_arrive_remote(map_rank(acce_bar(buf), 0));
-                    else mbar_arrive(acce_bar(buf));
+                } else {
+#pragma unroll
+                    for (int l = 0; l + 1 < kLoads; ++l)
+                        if (l < loads) {
+                            uint32_t r[16];
+                            tmem_ld16_start(addr(l), r);
+                            tmem_ld16_wait(r);
+                            add(r, l);
+                        }
+                    release();
                 }
             }
             if (!ok) break;
-            if constexpr (P::kLower) store_gram(g, x, lane_row, col0, acc);
-            else if (g.out_type == BAKRON_BF16) store_tile<P, __nv_bfloat16>(g, x, lane_row, col0, acc);
+            if (P::kEight && P::kRagged == kTokensA && g.w_step_rows == 1) {
+                // one step per column, through shared memory (a warp's own)
+                const float *s = g.w_steps + (int64_t)x.e * g.b_total + x.b0 + col0;
+                __syncwarp();
+                for (int j = lane; j < S::kCols; j += 32) steps_w[j] = col0 + j < x.nb ? __ldg(s + j) : 0.f;
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < S::kCols / 2; ++c) mul2(acc[c], *(const uint64_t *)(steps_w + 2 * c));
+            }
+            if constexpr (P::kLower) {
+                store_gram(g, x, lane_row, col0, acc);
+                continue;
+            }
+            if constexpr (S::kTurn) {
+                if (g.turn) {
+                    const int thread = quad * 32 + lane;
+                    if (g.out_type == BAKRON_BF16)
+                        store_turned<P>(g, x, rank, thread, half, acc, (__nv_bfloat16 *)(turn_sh + half * kTurnBytes));
+                    else
+                        store_turned<P>(g, x, rank, thread, half, acc, (__half *)(turn_sh + half * kTurnBytes));
+                    continue;
+                }
+            }
+            if (g.out_type == BAKRON_BF16) store_tile<P, __nv_bfloat16>(g, x, lane_row, col0, acc);
             else if (g.out_type == BAKRON_F16) store_tile<P, __half>(g, x, lane_row, col0, acc);
             else store_tile<P, float>(g, x, lane_row, col0, acc);
         }
