@@ -980,6 +980,7 @@ bakron_status_t bakron_get_status(void *ws_dev, size_t ws_bytes, bakron_stream_t
     if (cudaStreamSynchronize(s) != cudaSuccess) return BAKRON_ERR_CUDA;
     DeviceStatus h;
     if (cudaMemcpy(&h, ws_dev, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return BAKRON_ERR_CUDA;
+    for (int i = 0; i < kStatusSlots && h.code == 0; ++i) h.code = h.slots[i];
     if (h.code != 0 && cudaMemset(ws_dev, 0, sizeof(h)) != cudaSuccess) return BAKRON_ERR_CUDA;
     return (bakron_status_t)h.code;
 }

@@ -18,8 +18,9 @@ constexpr int kTile = 128;
 struct DeviceStatus {
     int32_t code;      // first recorded bakron_status_t (0 = ok)
     int32_t where;     // kernel-specific location (index of the offending item)
-    int32_t pad[62];
+    uint8_t slots[248];  // or one code per CTA, from kernels that report so (0 = ok)
 };
+constexpr int kStatusSlots = 248;
 constexpr size_t kStatusBytes = 256;
 static_assert(sizeof(DeviceStatus) == kStatusBytes, "status block size");
 

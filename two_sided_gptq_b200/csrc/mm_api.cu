@@ -47,8 +47,9 @@ cudaError_t configure_device(int &sms)
     return cudaSuccess;
 }
 
-// Status block, cleared before the call's kernels.
-bakron_status_t begin(void *ws, size_t ws_bytes, size_t need, cudaStream_t stream, Args &g)
+// Workspace and time limit.  The status block is cleared here unless the call's
+// first kernel writes all of it.
+bakron_status_t begin(void *ws, size_t ws_bytes, size_t need, bool clear, cudaStream_t stream, Args &g)
 {
     if (!ws || ws_bytes < need) return BAKRON_ERR_WORKSPACE;
     if (!aligned16(ws)) return BAKRON_ERR_ALIGNMENT;
@@ -56,7 +57,8 @@ bakron_status_t begin(void *ws, size_t ws_bytes, size_t need, cudaStream_t strea
     if (!default_timeout_ms(ms)) return BAKRON_ERR_INVALID_ARG;
     g.timeout_ns = (uint64_t)ms * 1000000ull;
     g.st = (DeviceStatus *)ws;
-    if (cudaMemsetAsync(ws, 0, kStatusBytes, stream) != cudaSuccess) return BAKRON_ERR_CUDA;
+    g.split = 1;
+    if (clear && cudaMemsetAsync(ws, 0, kStatusBytes, stream) != cudaSuccess) return BAKRON_ERR_CUDA;
     return BAKRON_OK;
 }
 
@@ -109,6 +111,17 @@ int64_t row_tiles(int64_t rows, int64_t experts, int64_t tile)
     return rows / tile + (experts < rows ? experts : rows);
 }
 
+// CTAs per tile of a call with short groups: while the tiles would leave half
+// the SMs idle the contraction is split, down to two stages a CTA, as long as
+// the other parts' sums fit the first CTA's ring (192 KB of it).
+int split_of(int64_t tiles, int64_t stages, int64_t rows, int sms)
+{
+    const int64_t part_bytes = ceil64(rows < 64 ? rows : 64, 16) * 16 * 128 * 4;
+    int s = 1;
+    while (s < 8 && tiles * s * 2 <= sms && stages >= 4 * s && (2 * s - 1) * part_bytes <= 192 * 1024) s *= 2;
+    return s;
+}
+
 // y[t, :] = x[t, :] w_e^T (columns = false: contraction over w's columns) or
 // x[t, :] w_e (columns = true: over w's rows).
 bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t ldx, const void *w, int64_t ldw,
@@ -138,7 +151,7 @@ bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t 
     int sms = 0;
     if (configure_device(sms) != cudaSuccess) return BAKRON_ERR_CUDA;
     Args g{};
-    if ((s = begin(ws, ws_bytes, kStatusBytes, (cudaStream_t)stream, g)) != BAKRON_OK) return s;
+    if ((s = begin(ws, ws_bytes, kStatusBytes, !rows, (cudaStream_t)stream, g)) != BAKRON_OK) return s;
     if (!rows) return BAKRON_OK;
     g.offsets = offsets;
     g.experts = (int)experts;
@@ -149,6 +162,7 @@ bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t 
     g.ldo = ldy;
     g.out_type = y_type;
     g.turn = y_type != BAKRON_F32 && ldy % 8 == 0;
+    if (small) g.split = split_of(tiles, ceil64(in, 64), rows, sms);
     g.idesc = idesc16(type, columns, false);
     Maps m;
     const CUtensorMapDataType t = map_type(type);
@@ -193,7 +207,7 @@ bakron_status_t bakron_quantize_blocks(const void *x_dev, int32_t x_type, int64_
     if (!aligned16(x_dev) || !aligned16(q_dev) || !aligned16(scales_dev) || q_row_stride % 16)
         return BAKRON_ERR_ALIGNMENT;
     Args g{};
-    const bakron_status_t s = begin(ws_dev, ws_bytes, kStatusBytes, (cudaStream_t)stream, g);
+    const bakron_status_t s = begin(ws_dev, ws_bytes, kStatusBytes, true, (cudaStream_t)stream, g);
     if (s != BAKRON_OK || !blocks) return s;
     const QuantArgs a{x_dev, x_type, batch, rows, cols, x_batch_stride, x_row_stride, block_rows,
                       q_dev, q_row_stride, scales_dev, g.st};
@@ -230,7 +244,7 @@ bakron_status_t bakron_matmul_blocks(const uint8_t *x_dev, int64_t x_row_stride,
     int sms = 0;
     if (configure_device(sms) != cudaSuccess) return BAKRON_ERR_CUDA;
     Args g{};
-    if ((s = begin(ws_dev, ws_bytes, kStatusBytes, (cudaStream_t)stream, g)) != BAKRON_OK) return s;
+    if ((s = begin(ws_dev, ws_bytes, kStatusBytes, !rows, (cudaStream_t)stream, g)) != BAKRON_OK) return s;
     if (!rows) return BAKRON_OK;
     g.offsets = offsets_dev;
     g.experts = (int)experts;
@@ -245,6 +259,7 @@ bakron_status_t bakron_matmul_blocks(const uint8_t *x_dev, int64_t x_row_stride,
     g.x_steps = x_scales_dev;
     g.w_steps = w_scales_dev;
     g.w_step_rows = w_scale_rows;
+    if (small) g.split = split_of(tiles, ceil64(k, 128), rows, sms);
     Maps m;
     const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     CUtensorMap *xm = small ? &m.b : &m.a, *wm = small ? &m.a : &m.b;
@@ -297,7 +312,7 @@ bakron_status_t bakron_matmul_grouped_dw(const void *dy_dev, int32_t type, int64
     int sms = 0;
     if (configure_device(sms) != cudaSuccess) return BAKRON_ERR_CUDA;
     Args g{};
-    if ((s = begin(ws_dev, ws_bytes, kStatusBytes, (cudaStream_t)stream, g)) != BAKRON_OK) return s;
+    if ((s = begin(ws_dev, ws_bytes, kStatusBytes, !rows, (cudaStream_t)stream, g)) != BAKRON_OK) return s;
     if (!rows) {
         const size_t bytes = (size_t)experts * n * k * type_size(dw_type);
         return cudaMemsetAsync(dw_dev, 0, bytes, (cudaStream_t)stream) == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA;
@@ -357,7 +372,7 @@ bakron_status_t bakron_gram_grouped(const void *X_dev, int32_t type, int64_t x_r
     if (configure_device(sms) != cudaSuccess) return BAKRON_ERR_CUDA;
     cudaStream_t st = (cudaStream_t)stream;
     Args g{};
-    if ((s = begin(ws_dev, ws_bytes, L.total, st, g)) != BAKRON_OK) return s;
+    if ((s = begin(ws_dev, ws_bytes, L.total, !rows, st, g)) != BAKRON_OK) return s;
     if (!rows)
         return cudaMemsetAsync(A_dev, 0, (size_t)experts * d * d * 4, st) == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA;
     g.offsets = offsets_dev;

@@ -68,6 +68,8 @@ struct Shape {
     static constexpr int kCols = P::kBN / (kEpiWarps / 4);          // columns per epilogue thread
     // a warp's staged steps: two chunks of its columns' (kTokensB), or one of them
     static constexpr int kStepFloats = P::kRagged == kTokensB ? 2 * kCols : kCols;
+    // tiles whose contraction a cluster may split (few tiles, one per cluster)
+    static constexpr bool kSplit = P::kRagged == kTokensB && !P::kPair;
     static constexpr int kRing = 227 * 1024 - kReserve - kTurnSpace;
     static constexpr int kStages = kRing / kStageBytes < 8 ? kRing / kStageBytes : 8;
     static constexpr int kAcc = P::kPlanes > 1 ? 2 : 1;             // accumulators per buffer
@@ -361,8 +363,21 @@ __device__ __forceinline__ void zero_tail(uint8_t *stage, int valid, int steps, 
     __syncwarp();
 }
 
+// Every CTA reports in a byte of its own, so that no call needs the status
+// block cleared first: the first CTA clears the recorded code and the bytes
+// that no CTA of this grid owns.
+__device__ __forceinline__ void report(DeviceStatus *st, int error)
+{
+    if (blockIdx.x == 0) {
+        st->code = 0;
+        st->where = 0;
+        for (int i = gridDim.x; i < kStatusSlots; ++i) st->slots[i] = 0;
+    }
+    st->slots[blockIdx.x] = (uint8_t)error;
+}
+
 template <class P>
-__global__ void __cluster_dims__(P::kPair ? 2 : 1, 1, 1) __launch_bounds__(Shape<P>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<P>::kThreads, 1)
 mm_kernel(const __grid_constant__ Maps maps, const Args g)
 {
     using S = Shape<P>;
@@ -375,10 +390,13 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     int *first = (int *)(bars + 48);                        // tile numbering: kMaxExperts + 1
     float *steps_sh = (float *)(first + kMaxExperts + 4);   // staged row steps (kTokensB, 8-bit)
     __shared__ uint32_t tmem_base_sh;
-    __shared__ int abort_sh;
+    __shared__ int abort_sh, error_sh;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = kPair ? (int)cluster_rank() : 0;
+    // Split contraction: the CTAs of a cluster share one tile, each taking a
+    // part of its stages; one tile per cluster.
+    const int split = S::kSplit ? g.split : 1, part = S::kSplit && split > 1 ? (int)cluster_rank() : 0;
     const uint32_t bar0 = smem_u32(bars);
     // Barriers.  In a pair, full, accumulator-empty and tail-done barriers are
     // the first CTA's; the others each CTA has for itself.
@@ -407,6 +425,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             }
         mbar_init(drain_bar, 1);
         abort_sh = 0;
+        error_sh = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -431,7 +450,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             int n = 0;
             if (e < g.experts) {
                 int lo, hi;
-                if (!group_range(g, e, lo, hi) && blockIdx.x == 0) record_error(g.st, BAKRON_ERR_INVALID_ARG, e);
+                if (!group_range(g, e, lo, hi)) error_sh = BAKRON_ERR_INVALID_ARG;
                 n = P::kRagged == kContract ? fixed : tiles_of_group<P>(g, hi - lo);
             }
             int inc = n;
@@ -451,12 +470,16 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     tc_fence_after();
     const uint32_t tmem_base = tmem_base_sh;
     const int total = first[g.experts];
-    const int tile0 = blockIdx.x / S::kCtas, tile_step = gridDim.x / S::kCtas;
+    const int tile0 = blockIdx.x / (S::kCtas * split), tile_step = gridDim.x / (S::kCtas * split);
+    // this CTA's stages of a tile with n of them
+    auto stage_begin = [&](int n) { return S::kSplit ? n * part / split : 0; };
+    auto stage_end = [&](int n) { return S::kSplit ? n * (part + 1) / split : n; };
     volatile int *abort_flag = &abort_sh;
+    bool joined = false;
 
     // Bounded wait: false once it has run for the time limit or another role
     // has given up.
-    auto wait = [&](uint32_t bar, uint32_t parity, int where) -> bool {
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
         if (mbar_try_wait(bar, parity)) return true;
         const uint64_t t0 = now_ns();
         for (;;) {
@@ -464,7 +487,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                 if (mbar_try_wait(bar, parity)) return true;
             if (*abort_flag) return false;
             if (now_ns() - t0 > g.timeout_ns) {
-                record_error(g.st, BAKRON_ERR_DEVICE_TIMEOUT, where);
+                error_sh = BAKRON_ERR_DEVICE_TIMEOUT;
                 atomicExch(&abort_sh, 1);
                 return false;
             }
@@ -488,9 +511,9 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                 const int b0 = x.b0 + rank * share;
                 const int boxes = P::kRagged == kTokensB ? ceil_div(share, P::kBoxRows) : 1;
                 const uint32_t bytes = P::kRagged == kTokensB ? S::kABytes + boxes * P::kBoxRows * 128 : S::kStageBytes;
-                for (int kb = 0; kb < nkb; ++kb, ++it) {
+                for (int kb = stage_begin(nkb); kb < stage_end(nkb); ++kb, ++it) {
                     const int s = it % S::kStages;
-                    if (it >= S::kStages && !wait(empty_bar(s), (it / S::kStages - 1) & 1, 1000)) {
+                    if (it >= S::kStages && !wait(empty_bar(s), (it / S::kStages - 1) & 1)) {
                         ok = false;
                         break;
                     }
@@ -596,12 +619,13 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                 const int nkb = ceil_div(x.k1 - x.k0, S::kKB);
                 const int n_mma = P::kRagged == kTokensB ? (x.nb + 15) & ~15 : BN / S::kHalves;
                 const uint32_t idesc = g.idesc | ((uint32_t)(n_mma >> 3) << 17) | ((uint32_t)(S::kM >> 4) << 24);
-                for (int kb = 0; kb < nkb; ++kb, ++it) {
-                    const int buf = chunk & 1, in_chunk = kb % P::kChunk;
+                const int kb0 = stage_begin(nkb), kb1 = stage_end(nkb);
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int buf = chunk & 1, in_chunk = (kb - kb0) % P::kChunk;
                     const int s = it % S::kStages;
                     if (S::kHalves == 1 && in_chunk == 0 && chunk >= 2)
-                        ok = wait(acce_bar(buf, 0), ((chunk >> 1) - 1) & 1, 2000);
-                    ok = ok && wait(full_bar(s), (it / S::kStages) & 1, 2001);
+                        ok = wait(acce_bar(buf, 0), ((chunk >> 1) - 1) & 1);
+                    ok = ok && wait(full_bar(s), (it / S::kStages) & 1);
                     int steps = kSteps;
                     if (P::kRagged == kContract) {
                         const int valid = min(S::kKB, x.k1 - (x.k0 + kb * S::kKB));
@@ -609,7 +633,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                         if (valid & 15) {
                             // (the zeroes written there are ordered by an
                             // acquire at cluster scope once they are complete)
-                            ok = ok && wait(tail_done_bar(s), (tail_parity >> s) & 1, 2002) &&
+                            ok = ok && wait(tail_done_bar(s), (tail_parity >> s) & 1) &&
                                  mbar_try_wait_cluster(tail_done_bar(s), (tail_parity >> s) & 1);
                             tail_parity ^= 1u << s;
                         }
@@ -622,7 +646,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                     if constexpr (S::kHalves > 1) {
 #pragma unroll
                         for (int h = 0; h < S::kHalves; ++h) {
-                            ok = ok && (chunk < 2 || wait(acce_bar(buf, h), ((chunk >> 1) - 1) & 1, 2000));
+                            ok = ok && (chunk < 2 || wait(acce_bar(buf, h), ((chunk >> 1) - 1) & 1));
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
@@ -655,7 +679,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                             }
                         }
                         commit(empty_bar(s));
-                        if (in_chunk == P::kChunk - 1 || kb == nkb - 1) {
+                        if (in_chunk == P::kChunk - 1 || kb == kb1 - 1) {
                             commit(accf_bar(buf, 0));
                             ++chunk;
                         }
@@ -679,7 +703,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                 const int valid = (x.k1 - x.k0) % S::kKB;
                 if (!(valid & 15)) continue;
                 const int s = (it - 1) % S::kStages;
-                if (!__all_sync(0xffffffffu, wait(tail_full_bar(s), (tail_parity >> s) & 1, 2003))) break;
+                if (!__all_sync(0xffffffffu, wait(tail_full_bar(s), (tail_parity >> s) & 1))) break;
                 tail_parity ^= 1u << s;
                 zero_tail<P>(smem + s * S::kStageBytes, valid, (valid + 15) >> 4, lane);
                 if (lane == 0) {
@@ -704,7 +728,8 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
         for (int t = tile0; t < total && ok; t += tile_step) {
             const Tile x = find_tile<P>(g, first, t);
             const int nkb = ceil_div(x.k1 - x.k0, S::kKB);
-            const int nchunk = ceil_div(nkb, P::kChunk);
+            const int kb0 = stage_begin(nkb);
+            const int nchunk = ceil_div(stage_end(nkb) - kb0, P::kChunk);
             // 16-column loads of each chunk: the tile's valid columns only
             const int loads = min(max(ceil_div(x.nb - col0, 16), 0), S::kCols / 16) * S::kAcc;
             uint64_t acc[S::kCols / 2];  // packed pairs of FP32 columns
@@ -754,12 +779,12 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                 }
                 float *steps = steps_w + (c & 1) * S::kCols;
                 if (P::kEight && P::kRagged == kTokensB) {
-                    const float s = ws ? __ldg(ws + c) : 1.f;
+                    const float s = ws ? __ldg(ws + kb0 + c) : 1.f;
                     for (int j = lane; j < S::kCols; j += 32)
-                        steps[j] = col0 + j < x.nb ? __ldg(g.x_steps + (int64_t)(x.b0 + col0 + j) * nkb + c) * s : 0.f;
+                        steps[j] = col0 + j < x.nb ? __ldg(g.x_steps + (int64_t)(x.b0 + col0 + j) * nkb + kb0 + c) * s : 0.f;
                     __syncwarp();
                 }
-                ok = __all_sync(0xffffffffu, wait(accf_bar(buf, bar_half), (chunk >> 1) & 1, 3000));
+                ok = __all_sync(0xffffffffu, wait(accf_bar(buf, bar_half), (chunk >> 1) & 1));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t src = tmem_base + lane_off + (uint32_t)(buf * S::kAcc * BN + col0);
@@ -810,6 +835,30 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                     release();
                 }
             }
+            if constexpr (S::kSplit) {
+                if (split > 1) {
+                    // every part's MMAs have read their stages: the first CTA's
+                    // ring takes the other parts' sums, added in their order
+                    cluster_sync();
+                    float *slot = (float *)smem + quad * 32 + lane + (int64_t)col0 * kBM;
+                    const int part_floats = ((min(x.nb, BN) + 15) & ~15) * kBM;
+                    if (part) {
+                        const uint32_t dst = map_rank(smem_u32(slot + (part - 1) * part_floats), 0);
+#pragma unroll
+                        for (int c = 0; c < S::kCols; ++c)
+                            if (c < 16 * loads) store_cluster(dst + c * (kBM * 4), element(acc, c));
+                    }
+                    cluster_sync();
+                    joined = true;
+                    if (part) break;
+                    for (int p = 0; p < split - 1; ++p) {
+                        const float *from = slot + p * part_floats;
+#pragma unroll
+                        for (int c = 0; c < S::kCols; c += 2)
+                            if (c < 16 * loads) add2(acc[c / 2], pack2(from[c * kBM], from[(c + 1) * kBM]));
+                    }
+                }
+            }
             if (!ok) break;
             if (P::kEight && P::kRagged == kTokensA && g.w_step_rows == 1) {
                 // one step per column, through shared memory (a warp's own)
@@ -839,8 +888,17 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             else store_tile<P, float>(g, x, lane_row, col0, acc);
         }
     }
+    if constexpr (S::kSplit) {
+        // warps that have not taken part in the join arrive at its barriers
+        __syncwarp();
+        if (split > 1 && !joined) {
+            cluster_sync();
+            cluster_sync();
+        }
+    }
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0) report(g.st, error_sh);
     if (kPair) cluster_sync();  // neither CTA leaves while the other can still reach its memory
     if (warp == 1) {
         tc_fence_after();
@@ -872,9 +930,20 @@ template <class P>
 cudaError_t launch(const Maps &maps, const Args &g, int64_t tiles, int sms, cudaStream_t stream)
 {
     using S = Shape<P>;
-    const int64_t groups = min64(tiles, sms / S::kCtas);
-    mm_kernel<P><<<(unsigned)(groups * S::kCtas), S::kThreads, S::kSmem, stream>>>(maps, g);
-    return cudaGetLastError();
+    const int64_t groups = min64(tiles, min64(sms, kStatusSlots) / S::kCtas);  // (a split call has fewer tiles)
+    const int cluster = S::kSplit ? g.split : S::kCtas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(groups * cluster));
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, mm_kernel<P>, maps, g);
 }
 
 }  // namespace mm
