@@ -342,15 +342,30 @@ def _types():
 
 def _here(t, name, dims, dtypes):
     """A CUDA tensor on the current device with unit stride along its last dimension."""
+    try:
+        if (t.dtype in dtypes and t.dim() in dims and t.get_device() == _raw()._cuda_getDevice()
+                and (t.stride(-1) == 1 or t.shape[-1] <= 1)):
+            return t
+    except AttributeError:
+        pass
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes or t.dim() not in dims:
         raise TypeError(f"{name} must be a CUDA tensor of {' or '.join(map(str, dims))} dimensions and type "
                         f"{', '.join(str(d) for d in dtypes)}")
-    if t.device.index != torch._C._cuda_getDevice():
+    if t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}, not on the current device")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must have unit stride along its last dimension")
-    return t
+    raise ValueError(f"{name} must have unit stride along its last dimension")
+
+
+_raw_module = None
+
+
+def _raw():
+    """torch's binding module (the calls below are made once per product)."""
+    global _raw_module
+    if _raw_module is None:
+        _raw_module = _torch()._C
+    return _raw_module
 
 
 def _ld(t, dim, least, align):

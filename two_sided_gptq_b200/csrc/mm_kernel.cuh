@@ -441,6 +441,10 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         }
     }
+    // the next kernel's CTAs may start their own set-up; everything below may
+    // touch what earlier kernels wrote
+    pdl_trigger();
+    pdl_wait();
     if (warp == 2) {
         // tile numbering: exclusive prefix sum of the groups' tile counts
         int base = 0;
@@ -937,12 +941,14 @@ cudaError_t launch(const Maps &maps, const Args &g, int64_t tiles, int sms, cuda
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, mm_kernel<P>, maps, g);
 }
 

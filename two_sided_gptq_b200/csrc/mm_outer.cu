@@ -30,6 +30,8 @@ struct Gram {
 __global__ void split_three_kernel(const float *__restrict__ x, int64_t rows, int64_t d, int64_t ldx,
                                    __nv_bfloat16 *__restrict__ out, int64_t ld)
 {
+    pdl_wait();
+    pdl_trigger();
     const int64_t plane = rows * ld, n = rows * d;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t r = i / d, c = i - r * d;
@@ -50,6 +52,8 @@ __global__ void split_three_kernel(const float *__restrict__ x, int64_t rows, in
 // their squares overflow): recorded as BAKRON_ERR_NONFINITE.
 __global__ void gram_damp_kernel(float *__restrict__ A, int64_t d, float damping, DeviceStatus *st)
 {
+    pdl_wait();
+    pdl_trigger();
     __shared__ double part[32];
     __shared__ float add_sh;
     float *a = A + (int64_t)blockIdx.x * d * d;
@@ -96,14 +100,13 @@ cudaError_t launch_split_three(const float *x, int64_t rows, int64_t d, int64_t 
                                cudaStream_t stream)
 {
     const int64_t blocks = min64((rows * d + 1023) / 1024, 148 * 8);
-    split_three_kernel<<<(unsigned)blocks, 256, 0, stream>>>(x, rows, d, ldx, (__nv_bfloat16 *)planes, ld);
-    return cudaGetLastError();
+    return launch_pdl(split_three_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, x, rows, d, ldx,
+                      (__nv_bfloat16 *)planes, ld);
 }
 
 cudaError_t launch_gram_damp(float *A, int64_t d, int experts, float damping, DeviceStatus *st, cudaStream_t stream)
 {
-    gram_damp_kernel<<<experts, 256, 0, stream>>>(A, d, damping, st);
-    return cudaGetLastError();
+    return launch_pdl(gram_damp_kernel, dim3(experts), dim3(256), 0, stream, A, d, damping, st);
 }
 
 }  // namespace mm
