@@ -340,32 +340,36 @@ def _types():
     return _type_ids
 
 
-def _here(t, name, dims, dtypes):
-    """A CUDA tensor on the current device with unit stride along its last dimension."""
+_raw_module = None
+
+
+def _device():
+    """The current device's index (asked once per call, through torch's binding
+    module: the checks of a small product would otherwise cost more than it)."""
+    global _raw_module
+    if _raw_module is None:
+        torch = _torch()
+        if not torch.cuda.is_available():
+            return None  # no tensor is on it
+        _raw_module = torch._C
+    return _raw_module._cuda_getDevice()
+
+
+def _here(t, name, dims, dtypes, dev):
+    """A CUDA tensor on device ``dev`` with unit stride along its last dimension."""
     try:
-        if (t.dtype in dtypes and t.dim() in dims and t.get_device() == _raw()._cuda_getDevice()
+        if (t.dtype in dtypes and t.dim() in dims and t.get_device() == dev
                 and (t.stride(-1) == 1 or t.shape[-1] <= 1)):
-            return t
+            return
     except AttributeError:
         pass
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes or t.dim() not in dims:
         raise TypeError(f"{name} must be a CUDA tensor of {' or '.join(map(str, dims))} dimensions and type "
                         f"{', '.join(str(d) for d in dtypes)}")
-    if t.get_device() != torch._C._cuda_getDevice():
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on the current device")
     raise ValueError(f"{name} must have unit stride along its last dimension")
-
-
-_raw_module = None
-
-
-def _raw():
-    """torch's binding module (the calls below are made once per product)."""
-    global _raw_module
-    if _raw_module is None:
-        _raw_module = _torch()._C
-    return _raw_module
 
 
 def _ld(t, dim, least, align):
@@ -373,42 +377,40 @@ def _ld(t, dim, least, align):
     return t.stride(dim) if t.shape[dim] > 1 else -(-least // align) * align
 
 
-def _groups(offsets, experts=None):
-    torch = _torch()
-    _here(offsets, "offsets", (1,), (torch.int32,))
-    if offsets.shape[0] < 2 or (experts is not None and offsets.shape[0] != experts + 1):
+def _groups(offsets, dev, experts=None):
+    _here(offsets, "offsets", (1,), (_torch().int32,), dev)
+    n = offsets.shape[0]
+    if n < 2 or (experts is not None and n != experts + 1):
         raise ValueError("offsets must hold one bound more than there are experts")
-    if not offsets.is_contiguous():
-        raise ValueError("offsets must be contiguous")
-    return offsets.shape[0] - 1
+    return n - 1
 
 
-def _result(out, shape, dtype, allowed, device):
+def _result(out, shape, dtype, allowed, dev):
     """The result tensor: ``out``, or a new one of ``dtype``."""
-    torch = _torch()
     if out is None:
         if dtype not in allowed:
             raise TypeError(f"out_dtype must be one of {', '.join(str(d) for d in allowed)}")
-        return torch.empty(shape, dtype=dtype, device=device)
-    _here(out, "out", (len(shape),), allowed)
-    if tuple(out.shape) != tuple(shape) or (dtype is not None and out.dtype != dtype):
-        raise ValueError(f"out must have shape {tuple(shape)}" + (f" and type {dtype}" if dtype is not None else ""))
+        torch = _torch()
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    _here(out, "out", (len(shape),), allowed, dev)
+    if out.shape != shape or (dtype is not None and out.dtype != dtype):
+        raise ValueError(f"out must have shape {shape}" + (f" and type {dtype}" if dtype is not None else ""))
     return out
 
 
-def _call(name, args, ws, stream, check_status, device, need=STATUS_BYTES):
+def _call(name, args, ws, stream, check_status, dev, need=STATUS_BYTES):
     """One library call on a workspace: ``ws``, or a new one."""
-    torch = _torch()
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-    else:
-        _here(ws, "ws", (1,), (torch.uint8,))
-    st = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-    status = getattr(_lib(), name)(*args, ws.data_ptr(), ws.numel(), st)
+        ws = workspace(need, dev)
+    elif ws.get_device() != dev or ws.dtype != _torch().uint8 or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous uint8 tensor on the current device")
+    lib, at, size = _lib(), ws.data_ptr(), ws.numel()
+    st = _raw_module._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    status = getattr(lib, name)(*args, at, size, st)
     if status:
         check(status, name)
     if check_status:
-        check(_lib().bakron_get_status(ws.data_ptr(), ws.numel(), st), name + " (device)")
+        check(lib.bakron_get_status(at, size, st), name + " (device)")
 
 
 def quantize_blocks(x, block_rows=1, *, out=None, ws=None, stream=None, check_status=True):
@@ -422,7 +424,8 @@ def quantize_blocks(x, block_rows=1, *, out=None, ws=None, stream=None, check_st
     of a wider buffer for odd widths), ``scales`` of shape ``[..., ceil(rows /
     block_rows), ceil(cols / 128)]``.  ``out`` may supply both."""
     torch = _torch()
-    _here(x, "x", (2, 3), tuple(_types()))
+    dev = _device()
+    _here(x, "x", (2, 3), _types(), dev)
     rows, cols = x.shape[-2:]
     batch = x.shape[0] if x.dim() == 3 else 1
     lead = tuple(x.shape[:-2])
@@ -434,9 +437,9 @@ def quantize_blocks(x, block_rows=1, *, out=None, ws=None, stream=None, check_st
         scales = torch.empty(steps, dtype=torch.float32, device=x.device)
     else:
         q, scales = out
-        _here(q, "codes", (x.dim(),), (torch.float8_e4m3fn,))
-        _here(scales, "scales", (x.dim(),), (torch.float32,))
-        if q.shape != x.shape or tuple(scales.shape) != steps or not scales.is_contiguous():
+        _here(q, "codes", (x.dim(),), (torch.float8_e4m3fn,), dev)
+        _here(scales, "scales", (x.dim(),), (torch.float32,), dev)
+        if q.shape != x.shape or scales.shape != steps or not scales.is_contiguous():
             raise ValueError(f"codes must have shape {tuple(x.shape)}, scales {steps} (contiguous)")
     ldq = _ld(q, -2, cols, 16)
     if x.dim() == 3 and batch > 1 and rows and q.stride(0) != rows * ldq:
@@ -444,7 +447,7 @@ def quantize_blocks(x, block_rows=1, *, out=None, ws=None, stream=None, check_st
     ldx = _ld(x, -2, cols, 1)
     _call("bakron_quantize_blocks",
           (x.data_ptr(), _types()[x.dtype], batch, rows, cols, x.stride(0) if batch > 1 else 0, ldx, block_rows,
-           q.data_ptr(), ldq, scales.data_ptr()), ws, stream, check_status, x.device)
+           q.data_ptr(), ldq, scales.data_ptr()), ws, stream, check_status, dev)
     return q, scales
 
 
@@ -465,49 +468,52 @@ def matmul_blocks(x, x_scales, w, w_scales, offsets=None, *, out_dtype=None, out
     ``out_dtype`` or ``out`` says float16 or float32."""
     torch = _torch()
     f8, f32 = (torch.float8_e4m3fn,), (torch.float32,)
-    _here(x, "x", (2,), f8), _here(x_scales, "x_scales", (2,), f32)
-    lead = () if offsets is None else (1,)
-    _here(w, "w", (2 + len(lead),), f8)
-    _here(w_scales, "w_scales", (1 + len(lead), 2 + len(lead)), f32)
+    dev = _device()
+    lead = 0 if offsets is None else 1
+    _here(x, "x", (2,), f8, dev), _here(x_scales, "x_scales", (2,), f32, dev)
+    _here(w, "w", (2 + lead,), f8, dev), _here(w_scales, "w_scales", (1 + lead, 2 + lead), f32, dev)
     rows, k = x.shape
-    n = w.shape[-2]
-    experts = 1 if offsets is None else _groups(offsets, w.shape[0])
-    per_row = w_scales.dim() == 1 + len(lead)
-    steps = tuple(w.shape[:-2]) + ((n,) if per_row else (-(-n // 128), -(-k // 128)))
-    if w.shape[-1] != k or tuple(x_scales.shape) != (rows, -(-k // 128)) or tuple(w_scales.shape) != steps:
+    n, kw = w.shape[-2:]
+    experts = _groups(offsets, dev, w.shape[0]) if lead else 1
+    kblocks = -(-k // 128)
+    per_row = w_scales.dim() == 1 + lead
+    steps = (n,) if per_row else (-(-n // 128), kblocks)
+    if kw != k or x_scales.shape != (rows, kblocks) or w_scales.shape != ((experts,) + steps if lead else steps):
         raise ValueError("x is rows x k with steps rows x ceil(k/128); w is n x k with steps ceil(n/128) x "
                          "ceil(k/128) or (n,), under one leading dimension when offsets are given")
     if not x_scales.is_contiguous() or not w_scales.is_contiguous():
         raise ValueError("x_scales and w_scales must be contiguous")
     if out is None and out_dtype is None:
         out_dtype = torch.bfloat16
-    y = _result(out, (rows, n), out_dtype, _types(), x.device)
+    y = _result(out, (rows, n), out_dtype, _types(), dev)
     ldw = _ld(w, -2, k, 16)
     _call("bakron_matmul_blocks",
           (x.data_ptr(), _ld(x, 0, k, 16), x_scales.data_ptr(), w.data_ptr(), ldw,
            w.stride(0) if experts > 1 else -(-n * ldw // 16) * 16, w_scales.data_ptr(), 1 if per_row else 128,
            offsets.data_ptr() if offsets is not None else 0, experts, y.data_ptr(), _types()[y.dtype],
-           _ld(y, 0, n, 1), rows, n, k), ws, stream, check_status, x.device)
+           _ld(y, 0, n, 1), rows, n, k), ws, stream, check_status, dev)
     return y
 
 
 def _grouped(name, x, w, offsets, across, out_dtype, out, ws, stream, check_status):
     torch = _torch()
-    _here(x, "x" if across == 2 else "dy", (2,), (torch.bfloat16, torch.float16))
-    _here(w, "w", (3,), (x.dtype,))
-    experts = _groups(offsets, w.shape[0])
-    n, k = w.shape[1:]
-    rows = x.shape[0]
-    if x.shape[1] != w.shape[across]:
-        raise ValueError(f"{'x' if across == 2 else 'dy'} must have {w.shape[across]} columns")
-    width = w.shape[3 - across]
+    dev = _device()
+    _here(x, "x" if across == 2 else "dy", (2,), (torch.bfloat16, torch.float16), dev)
+    dtype = x.dtype
+    _here(w, "w", (3,), (dtype,), dev)
+    experts, n, k = w.shape
+    _groups(offsets, dev, experts)
+    rows, into = x.shape
+    if into != (k if across == 2 else n):
+        raise ValueError(f"{'x' if across == 2 else 'dy'} must have {k if across == 2 else n} columns")
+    width = n if across == 2 else k
     if out is None and out_dtype is None:
-        out_dtype = x.dtype
-    y = _result(out, (rows, width), out_dtype, (x.dtype, torch.float32), x.device)
+        out_dtype = dtype
+    y = _result(out, (rows, width), out_dtype, (dtype, torch.float32), dev)
     ldw = _ld(w, 1, k, 8)
-    _call(name, (x.data_ptr(), _types()[x.dtype], _ld(x, 0, x.shape[1], 8), w.data_ptr(), ldw,
+    _call(name, (x.data_ptr(), _types()[dtype], _ld(x, 0, into, 8), w.data_ptr(), ldw,
                  w.stride(0) if experts > 1 else n * ldw, offsets.data_ptr(), experts, y.data_ptr(),
-                 _types()[y.dtype], _ld(y, 0, width, 1), rows, n, k), ws, stream, check_status, x.device)
+                 _types()[y.dtype], _ld(y, 0, width, 1), rows, n, k), ws, stream, check_status, dev)
     return y
 
 
@@ -531,21 +537,22 @@ def matmul_grouped_dw(dy, x, offsets, *, out_dtype=None, out=None, ws=None, stre
     dy[t]^T x[t]`` over expert e's rows, experts x n x k, zeros for an expert
     without rows (``bakron_matmul_grouped_dw``)."""
     torch = _torch()
-    _here(dy, "dy", (2,), (torch.bfloat16, torch.float16))
-    _here(x, "x", (2,), (dy.dtype,))
-    experts = _groups(offsets)
+    dev = _device()
+    _here(dy, "dy", (2,), (torch.bfloat16, torch.float16), dev)
+    _here(x, "x", (2,), (dy.dtype,), dev)
+    experts = _groups(offsets, dev)
     rows, n = dy.shape
     if x.shape[0] != rows:
         raise ValueError("dy and x must have the same rows")
     k = x.shape[1]
     if out is None and out_dtype is None:
         out_dtype = x.dtype
-    dw = _result(out, (experts, n, k), out_dtype, (x.dtype, torch.float32), x.device)
+    dw = _result(out, (experts, n, k), out_dtype, (x.dtype, torch.float32), dev)
     if not dw.is_contiguous():
         raise ValueError("out must be contiguous")
     _call("bakron_matmul_grouped_dw",
           (dy.data_ptr(), _types()[x.dtype], _ld(dy, 0, n, 8), x.data_ptr(), _ld(x, 0, k, 8), offsets.data_ptr(),
-           experts, dw.data_ptr(), _types()[dw.dtype], rows, n, k), ws, stream, check_status, x.device)
+           experts, dw.data_ptr(), _types()[dw.dtype], rows, n, k), ws, stream, check_status, dev)
     return dw
 
 
@@ -556,16 +563,17 @@ def gram_grouped(X, offsets, damping=0.0, *, ws=None, out=None, stream=None, che
     experts + 1, on the device); experts x d x d float32, zeros for an expert
     without rows (``bakron_gram_grouped``)."""
     torch = _torch()
-    _here(X, "X", (2,), tuple(_types()))
-    experts = _groups(offsets)
+    dev = _device()
+    _here(X, "X", (2,), _types(), dev)
+    experts = _groups(offsets, dev)
     rows, d = X.shape
-    A = _result(out, (experts, d, d), torch.float32, (torch.float32,), X.device)
+    A = _result(out, (experts, d, d), torch.float32, (torch.float32,), dev)
     if not A.is_contiguous():
         raise ValueError("out must be contiguous")
     t = _types()[X.dtype]
     need = _lib().bakron_gram_grouped_workspace_size(t, rows, d) if ws is None else 0
     _call("bakron_gram_grouped", (X.data_ptr(), t, _ld(X, 0, d, 8), offsets.data_ptr(), experts, float(damping),
-                                  A.data_ptr(), rows, d), ws, stream, check_status, X.device, need)
+                                  A.data_ptr(), rows, d), ws, stream, check_status, dev, need)
     return A
 
 
