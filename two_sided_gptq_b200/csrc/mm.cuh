@@ -30,6 +30,7 @@ struct Args {
     uint32_t idesc;                  // MMA instruction descriptor without M and N
     const float *x_steps, *w_steps;  // 8-bit operands' steps
     int w_step_rows;                 // rows per weight step: 128, or 1 (one step per row)
+    int chunk;                       // stages per accumulator chunk (16-bit operands)
     int split;                       // CTAs that share a tile's contraction (kernels that can split)
     DeviceStatus *st;
     uint64_t timeout_ns;

@@ -24,6 +24,13 @@ constexpr int64_t kMaxDim = (int64_t)1 << 30;
 constexpr int64_t kMaxStride = (int64_t)1 << 39;  // bytes; tensor maps take strides below 2^40
 constexpr int64_t kMaxTiles = (int64_t)1 << 30;
 
+// Stages (64 operand columns, or packed rows where those are the contraction; 32
+// from three bf16 parts) that one accumulator sums before it is added to FP32
+// registers.  The tensor cores truncate, so the sums of an FP32 result are kept
+// to 512 products: 4e-7 of the result for 4096 random products, against 2e-7 at
+// 256 and 2e-6 at 2048.  A 16-bit result rounds a thousand times more.
+constexpr int kChunkF32 = 8, kChunk16 = 16;
+
 std::mutex g_mu;
 int g_sms[64] = {};  // SM count of each configured device
 
@@ -164,6 +171,7 @@ bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t 
     g.turn = y_type != BAKRON_F32 && ldy % 8 == 0;
     if (small) g.split = split_of(tiles, ceil64(in, 64), rows, sms);
     g.idesc = idesc16(type, columns, false);
+    g.chunk = y_type == BAKRON_F32 ? kChunkF32 : kChunk16;
     Maps m;
     const CUtensorMapDataType t = map_type(type);
     if (!map3(&m.a, t, 2, w, k, n, ldw, experts, w_stride, 64, columns ? 64 : 128) ||
@@ -327,6 +335,7 @@ bakron_status_t bakron_matmul_grouped_dw(const void *dy_dev, int32_t type, int64
     g.out_expert_stride = n * k;
     g.out_type = dw_type;
     g.idesc = idesc16(type, true, true);
+    g.chunk = dw_type == BAKRON_F32 ? kChunkF32 : kChunk16;
     Maps m;
     const CUtensorMapDataType t = map_type(type);
     if (!map3(&m.a, t, 2, dy_dev, n, rows, dy_row_stride, 1, rows * dy_row_stride, 64, 64) ||
@@ -384,6 +393,7 @@ bakron_status_t bakron_gram_grouped(const void *X_dev, int32_t type, int64_t x_r
     g.ldo = d;
     g.out_expert_stride = d * d;
     g.out_type = BAKRON_F32;
+    g.chunk = kChunkF32;
     Maps m;
     if (type == BAKRON_F32) {
         uint16_t *planes = (uint16_t *)((char *)ws_dev + L.planes);

@@ -13,12 +13,12 @@ namespace {
 struct EightA {
     static constexpr Ragged kRagged = kTokensA;
     static constexpr bool kPair = true, kEight = true, kAColumns = false, kLower = false;
-    static constexpr int kBN = 256, kPlanes = 1, kChunk = 1, kKRows = 0, kBoxRows = 128;
+    static constexpr int kBN = 256, kPlanes = 1, kKRows = 0, kBoxRows = 128;
 };
 struct EightB {
     static constexpr Ragged kRagged = kTokensB;
     static constexpr bool kPair = false, kEight = true, kAColumns = false, kLower = false;
-    static constexpr int kBN = 64, kPlanes = 1, kChunk = 1, kKRows = 0, kBoxRows = 32;
+    static constexpr int kBN = 64, kPlanes = 1, kKRows = 0, kBoxRows = 32;
 };
 }  // namespace
 

@@ -25,9 +25,9 @@
 //
 // Warp roles: warp 0 lane 0 issues TMA into a ring of kStages stages; warp 1
 // owns TMEM and issues the MMAs; warps 4..11 read finished accumulator chunks
-// (kChunk stages each, double buffered in TMEM) and add them in FP32 registers,
+// (a few stages each, double buffered in TMEM) and add them in FP32 registers,
 // scaled by the 8-bit operands' steps where there are any.  The tensor cores'
-// accumulator truncates, so sums are kept to kChunk stages there.  Where the
+// accumulator truncates, so an FP32 result's sums are kept short there.  Where the
 // packed rows are the contraction, warp 3 zeroes what a group's last stage
 // holds beyond the group.
 // Every mbarrier wait is bounded; on expiry the CTA records
@@ -321,11 +321,14 @@ __device__ __forceinline__ void store_gram(const Args &g, const Tile &x, int lan
     const float count = (float)max(x.count, 1), rcount = __frcp_rn(count);
     auto value = [&](int c) { return div_rn_recip(element(acc, c), count, rcount); };
     float *row = out + i * d + j0, *col = out + j0 * d + i;
-    if (j0 + 2 * N <= x.a0 && ((uintptr_t)row & 31) == 0) {
-        // below the diagonal throughout: whole 32-byte sectors along the row,
-        // and a warp's 32 rows next to each other in the mirror image
+    const bool vec = ((uintptr_t)row & 31) == 0;
+    // Eight columns at a time: whole 32-byte sectors along the row where all
+    // eight are below the diagonal, and a warp's 32 rows next to each other in
+    // the mirror image.
 #pragma unroll
-        for (int c = 0; c < 2 * N; c += 8) {
+    for (int c = 0; c < 2 * N; c += 8) {
+        const int n = min(x.nb - col0, i + 1 - j0) - c;  // columns of these that are written
+        if (n >= 8 && vec) {
             uint32_t v[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
@@ -333,15 +336,14 @@ __device__ __forceinline__ void store_gram(const Args &g, const Tile &x, int lan
                 col[(int64_t)(c + u) * d] = __uint_as_float(v[u]);
             }
             store32(row + c, v);
-        }
-        return;
-    }
+        } else if (n > 0) {
 #pragma unroll
-    for (int c = 0; c < 2 * N; ++c) {
-        if (col0 + c < x.nb && j0 + c <= i) {
-            const float v = value(c);
-            row[c] = v;
-            col[(int64_t)c * d] = v;
+            for (int u = 0; u < 8; ++u)
+                if (u < n) {
+                    const float v = value(c + u);
+                    row[c + u] = v;
+                    col[(int64_t)(c + u) * d] = v;
+                }
         }
     }
 }
@@ -474,6 +476,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     tc_fence_after();
     const uint32_t tmem_base = tmem_base_sh;
     const int total = first[g.experts];
+    const int chunk_stages = P::kEight ? 1 : g.chunk;
     const int tile0 = blockIdx.x / (S::kCtas * split), tile_step = gridDim.x / (S::kCtas * split);
     // this CTA's stages of a tile with n of them
     auto stage_begin = [&](int n) { return S::kSplit ? n * part / split : 0; };
@@ -624,8 +627,8 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                 const int n_mma = P::kRagged == kTokensB ? (x.nb + 15) & ~15 : BN / S::kHalves;
                 const uint32_t idesc = g.idesc | ((uint32_t)(n_mma >> 3) << 17) | ((uint32_t)(S::kM >> 4) << 24);
                 const int kb0 = stage_begin(nkb), kb1 = stage_end(nkb);
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int buf = chunk & 1, in_chunk = (kb - kb0) % P::kChunk;
+                for (int kb = kb0, in_chunk = 0; kb < kb1; ++kb, ++it) {
+                    const int buf = chunk & 1;
                     const int s = it % S::kStages;
                     if (S::kHalves == 1 && in_chunk == 0 && chunk >= 2)
                         ok = wait(acce_bar(buf, 0), ((chunk >> 1) - 1) & 1);
@@ -683,8 +686,9 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                             }
                         }
                         commit(empty_bar(s));
-                        if (in_chunk == P::kChunk - 1 || kb == kb1 - 1) {
+                        if (++in_chunk == chunk_stages || kb == kb1 - 1) {
                             commit(accf_bar(buf, 0));
+                            in_chunk = 0;
                             ++chunk;
                         }
                     }
@@ -733,7 +737,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             const Tile x = find_tile<P>(g, first, t);
             const int nkb = ceil_div(x.k1 - x.k0, S::kKB);
             const int kb0 = stage_begin(nkb);
-            const int nchunk = ceil_div(stage_end(nkb) - kb0, P::kChunk);
+            const int nchunk = ceil_div(stage_end(nkb) - kb0, chunk_stages);
             // 16-column loads of each chunk: the tile's valid columns only
             const int loads = min(max(ceil_div(x.nb - col0, 16), 0), S::kCols / 16) * S::kAcc;
             uint64_t acc[S::kCols / 2];  // packed pairs of FP32 columns

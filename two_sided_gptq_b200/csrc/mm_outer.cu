@@ -16,13 +16,13 @@ namespace {
 struct Outer {
     static constexpr Ragged kRagged = kContract;
     static constexpr bool kPair = true, kEight = false, kAColumns = true, kLower = false;
-    static constexpr int kBN = 256, kPlanes = 1, kChunk = 4, kKRows = 64, kBoxRows = 64;
+    static constexpr int kBN = 256, kPlanes = 1, kKRows = 64, kBoxRows = 64;
 };
 template <int Planes>
 struct Gram {
     static constexpr Ragged kRagged = kContract;
     static constexpr bool kPair = true, kEight = false, kAColumns = true, kLower = true;
-    static constexpr int kBN = Planes > 1 ? 128 : 256, kPlanes = Planes, kChunk = 4, kKRows = Planes > 1 ? 32 : 64, kBoxRows = kKRows;
+    static constexpr int kBN = Planes > 1 ? 128 : 256, kPlanes = Planes, kKRows = Planes > 1 ? 32 : 64, kBoxRows = kKRows;
 };
 
 // Three bf16 parts of an fp32 matrix, each rounded to nearest from what the
