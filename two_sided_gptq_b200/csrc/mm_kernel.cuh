@@ -48,6 +48,7 @@ namespace mm {
 using namespace tc;
 
 constexpr int kBM = 128;
+constexpr int kMaxSorted = 128;  // groups up to which they are sorted by length
 constexpr int kReserve = 10 * 1024;  // barriers, tile numbering, alignment, staged steps
 
 template <class P>
@@ -133,7 +134,7 @@ __device__ __forceinline__ int tiles_of_group(const Args &g, int len)
 }
 
 template <class P>
-__device__ __forceinline__ Tile find_tile(const Args &g, const int *first, int t)
+__device__ __forceinline__ Tile find_tile(const Args &g, const int *first, const uint16_t *order, int t)
 {
     constexpr int kM = Shape<P>::kM;
     int a = 0, b = g.experts;  // the last group whose first tile is <= t
@@ -143,9 +144,9 @@ __device__ __forceinline__ Tile find_tile(const Args &g, const int *first, int t
         else b = m;
     }
     Tile x;
-    x.e = a;
+    x.e = P::kRagged == kContract ? order[a] : a;
     int lo, hi;
-    group_range(g, a, lo, hi);
+    group_range(g, x.e, lo, hi);
     int i = t - first[a];
     x.count = hi - lo;
     if (P::kRagged == kTokensB) {
@@ -390,7 +391,8 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     uint8_t *turn_sh = smem + S::kStages * S::kStageBytes;
     uint64_t *bars = (uint64_t *)(turn_sh + S::kTurnSpace);
     int *first = (int *)(bars + 48);                        // tile numbering: kMaxExperts + 1
-    float *steps_sh = (float *)(first + kMaxExperts + 4);   // staged row steps (kTokensB, 8-bit)
+    uint16_t *order = (uint16_t *)(first + kMaxExperts + 4);  // groups, longest first (kContract)
+    float *steps_sh = (float *)(first + kMaxExperts + 4);     // staged row steps (8-bit)
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh, error_sh;
 
@@ -448,9 +450,25 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     pdl_trigger();
     pdl_wait();
     if (warp == 2) {
-        // tile numbering: exclusive prefix sum of the groups' tile counts
+        // tile numbering: exclusive prefix sum of the groups' tile counts;
+        // where a tile's cost is its group's length, longest groups first
         int base = 0;
         const int fixed = P::kRagged == kContract ? tiles_of_group<P>(g, 0) : 0;
+        if (P::kRagged == kContract) {
+            for (int e = lane; e < g.experts; e += 32) {
+                int lo, hi, place = e;
+                group_range(g, e, lo, hi);
+                if (g.experts <= kMaxSorted) {
+                    place = 0;
+                    for (int o = 0; o < g.experts; ++o) {
+                        int a, b;
+                        group_range(g, o, a, b);
+                        place += b - a > hi - lo || (b - a == hi - lo && o < e);
+                    }
+                }
+                order[place] = (uint16_t)e;
+            }
+        }
         for (int e0 = 0; e0 < g.experts; e0 += 32) {
             const int e = e0 + lane;
             int n = 0;
@@ -478,6 +496,13 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     const int total = first[g.experts];
     const int chunk_stages = P::kEight ? 1 : g.chunk;
     const int tile0 = blockIdx.x / (S::kCtas * split), tile_step = gridDim.x / (S::kCtas * split);
+    // The tile after t.  Where a tile's cost is its group's length, every other
+    // round runs backwards, so that who had a long tile gets a short one.
+    auto next_tile = [&](int t) {
+        if (P::kRagged != kContract) return t + tile_step;
+        const int round = t / tile_step;
+        return round & 1 ? (round + 1) * tile_step + tile0 : (round + 2) * tile_step - 1 - tile0;
+    };
     // this CTA's stages of a tile with n of them
     auto stage_begin = [&](int n) { return S::kSplit ? n * part / split : 0; };
     auto stage_end = [&](int n) { return S::kSplit ? n * (part + 1) / split : n; };
@@ -509,8 +534,8 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             int it = 0;
             uint32_t tail_last = 0, tail_count = 0;  // per stage: last use was a tail; parity of its tails
             bool ok = true;
-            for (int t = tile0; t < total && ok; t += tile_step) {
-                const Tile x = find_tile<P>(g, first, t);
+            for (int t = tile0; t < total && ok; t = next_tile(t)) {
+                const Tile x = find_tile<P>(g, first, order, t);
                 const int nkb = ceil_div(x.k1 - x.k0, S::kKB);
                 const int a0 = x.a0 + rank * kBM;
                 // rows of B this CTA loads: its share of the instruction's N
@@ -621,8 +646,8 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                 if (kPair) umma_commit_pair(bar);
                 else umma_commit(bar);
             };
-            for (int t = tile0; t < total && ok; t += tile_step) {
-                const Tile x = find_tile<P>(g, first, t);
+            for (int t = tile0; t < total && ok; t = next_tile(t)) {
+                const Tile x = find_tile<P>(g, first, order, t);
                 const int nkb = ceil_div(x.k1 - x.k0, S::kKB);
                 const int n_mma = P::kRagged == kTokensB ? (x.nb + 15) & ~15 : BN / S::kHalves;
                 const uint32_t idesc = g.idesc | ((uint32_t)(n_mma >> 3) << 17) | ((uint32_t)(S::kM >> 4) << 24);
@@ -705,8 +730,8 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             // ---------------- zero the tails of this CTA's operands
             int it = 0;
             uint32_t tail_parity = 0;
-            for (int t = tile0; t < total; t += tile_step) {
-                const Tile x = find_tile<P>(g, first, t);
+            for (int t = tile0; t < total; t = next_tile(t)) {
+                const Tile x = find_tile<P>(g, first, order, t);
                 it += ceil_div(x.k1 - x.k0, S::kKB);
                 const int valid = (x.k1 - x.k0) % S::kKB;
                 if (!(valid & 15)) continue;
@@ -733,8 +758,8 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
         const uint32_t first_cta_acce = kPair ? map_rank(acce_bar(0, 0), 0) : acce_bar(0, 0);
         int chunk = 0;
         bool ok = true;
-        for (int t = tile0; t < total && ok; t += tile_step) {
-            const Tile x = find_tile<P>(g, first, t);
+        for (int t = tile0; t < total && ok; t = next_tile(t)) {
+            const Tile x = find_tile<P>(g, first, order, t);
             const int nkb = ceil_div(x.k1 - x.k0, S::kKB);
             const int kb0 = stage_begin(nkb);
             const int nchunk = ceil_div(stage_end(nkb) - kb0, chunk_stages);

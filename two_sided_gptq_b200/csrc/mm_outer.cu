@@ -26,23 +26,38 @@ struct Gram {
 };
 
 // Three bf16 parts of an fp32 matrix, each rounded to nearest from what the
-// earlier ones leave (those differences are exact in fp32).
-__global__ void split_three_kernel(const float *__restrict__ x, int64_t rows, int64_t d, int64_t ldx,
-                                   __nv_bfloat16 *__restrict__ out, int64_t ld)
+// earlier ones leave (those differences are exact in fp32).  A warp takes 256
+// columns of a row (grid x: eight rows a CTA, y: strips of columns), eight per
+// thread.  Bound by its 4 + 6 bytes per element.
+__global__ void __launch_bounds__(256) split_three_kernel(const float *__restrict__ x, int64_t rows, int64_t d,
+                                                          int64_t ldx, __nv_bfloat16 *__restrict__ out, int64_t ld)
 {
     pdl_wait();
     pdl_trigger();
-    const int64_t plane = rows * ld, n = rows * d;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t r = i / d, c = i - r * d;
-        const float v = x[r * ldx + c];
-        const __nv_bfloat16 h = __float2bfloat16_rn(v);
-        const float r1 = v - __bfloat162float(h);
-        const __nv_bfloat16 m = __float2bfloat16_rn(r1);
-        __nv_bfloat16 *o = out + r * ld + c;
-        o[0] = h;
-        o[plane] = m;
-        o[2 * plane] = __float2bfloat16_rn(r1 - __bfloat162float(m));
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), plane = rows * ld;
+    if (row >= rows) return;
+    const float *src = x + row * ldx;
+    const bool vec = ((uintptr_t)src & 15) == 0;
+    for (int64_t c = (int64_t)blockIdx.y * 256 + (threadIdx.x & 31) * 8; c < d; c += (int64_t)gridDim.y * 256) {
+        float v[8];
+        if (vec && c + 8 <= d) {
+            *(float4 *)v = __ldg((const float4 *)(src + c));
+            *(float4 *)(v + 4) = __ldg((const float4 *)(src + c + 4));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = c + i < d ? src[c + i] : 0.f;
+        }
+        // (a plane's rows are padded to eight columns)
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            __align__(16) __nv_bfloat16 h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                h[i] = __float2bfloat16_rn(v[i]);
+                v[i] -= __bfloat162float(h[i]);
+            }
+            *(uint4 *)(out + p * plane + row * ld + c) = *(const uint4 *)h;
+        }
     }
 }
 
@@ -99,14 +114,14 @@ cudaError_t launch_outer(Variant v, const Maps &maps, const Args &g, int64_t til
 cudaError_t launch_split_three(const float *x, int64_t rows, int64_t d, int64_t ldx, uint16_t *planes, int64_t ld,
                                cudaStream_t stream)
 {
-    const int64_t blocks = min64((rows * d + 1023) / 1024, 148 * 8);
-    return launch_pdl(split_three_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, x, rows, d, ldx,
+    const dim3 grid((unsigned)((rows + 7) / 8), (unsigned)min64((d + 255) / 256, 65535));
+    return launch_pdl(split_three_kernel, grid, dim3(256), 0, stream, x, rows, d, ldx,
                       (__nv_bfloat16 *)planes, ld);
 }
 
 cudaError_t launch_gram_damp(float *A, int64_t d, int experts, float damping, DeviceStatus *st, cudaStream_t stream)
 {
-    return launch_pdl(gram_damp_kernel, dim3(experts), dim3(256), 0, stream, A, d, damping, st);
+    return launch_pdl(gram_damp_kernel, dim3(experts), dim3(1024), 0, stream, A, d, damping, st);
 }
 
 }  // namespace mm
