@@ -104,14 +104,14 @@ __device__ __forceinline__ float step_of(float most)
     return s == 0.f ? 1.f : s;
 }
 
+// rs: 1 / s correctly rounded.
 template <typename T>
-__device__ __forceinline__ void store8(uint8_t *row, int64_t c, int64_t cols, const Eight<T> &e, float s)
+__device__ __forceinline__ void store8(uint8_t *row, int64_t c, int64_t cols, const Eight<T> &e, float s, float rs)
 {
     float v[8];
     to_floats(e, v);
     // div_rn_recip is exact for steps in [2^-60, 2^60] wherever the code is not zero
     if (s >= 0x1p-60f && s <= 0x1p60f) {
-        const float rs = __frcp_rn(s);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = div_rn_recip(v[i], s, rs);
     } else {
@@ -162,13 +162,18 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a)
         for (int o = 8; o; o >>= 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) most[i] = most2<T>(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
+        // the warp's eight steps: one per lane, then handed round (computed by
+        // every lane for itself, the divisions were a third of the instructions)
+        const uint32_t own = sub & 2 ? (sub & 1 ? most[3] : most[2]) : (sub & 1 ? most[1] : most[0]);
+        const float m = most_value<T>(own), s_own = step_of(m), rs_own = __frcp_rn(s_own);
+        finite &= isfinite(m);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t kb = strip * (kStrip / 128) + i * 2 + (lane >> 4), c = kb * 128 + sub * 8;
+            const float s = __shfl_sync(0xffffffffu, s_own, (lane & 16) | i);
+            const float rs = __shfl_sync(0xffffffffu, rs_own, (lane & 16) | i);
+            const int64_t kb = strip * (kStrip / 128) + i * 2 + (lane >> 4);
             if (kb < kblocks) {
-                const float m = most_value<T>(most[i]), s = step_of(m);
-                finite &= isfinite(m);
-                store8(dst, c, a.cols, v[i], s);
+                store8(dst, kb * 128 + sub * 8, a.cols, v[i], s, rs);
                 if (sub == 0) a.steps[row * kblocks + kb] = s;
             }
         }
@@ -206,11 +211,11 @@ __global__ void __launch_bounds__(kTileThreads, 2) quantize_tiles_kernel(const Q
     for (int i = 0; i < kTileThreads / 32; ++i) most = most2<T>(most, part[i]);
     const float m = most_value<T>(most);
     if (!isfinite(m) && threadIdx.x == 0) record_error(a.st, BAKRON_ERR_NONFINITE, (int)blockIdx.x);
-    const float s = step_of(m);
+    const float s = step_of(m), rs = __frcp_rn(s);
 #pragma unroll
     for (int i = 0; i < kTileLoads; ++i) {
         const int64_t r = (int64_t)rb * 128 + r0 + kTileRows * i;
-        if (r < a.rows) store8(a.q + ((int64_t)e * a.rows + r) * a.q_row_stride, c, a.cols, v[i], s);
+        if (r < a.rows) store8(a.q + ((int64_t)e * a.rows + r) * a.q_row_stride, c, a.cols, v[i], s, rs);
     }
     if (threadIdx.x == 0) a.steps[(int64_t)eb * kblocks + kb] = s;
 }
