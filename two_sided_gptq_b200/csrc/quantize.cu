@@ -24,7 +24,7 @@ struct alignas(16) Eight {
 
 // From column c on, zeros from column `cols` on.
 template <typename T>
-__device__ __forceinline__ Eight<T> load8(const T *row, int64_t c, int64_t cols, bool vec)
+__device__ __forceinline__ Eight<T> load8(const T *row, int c, int cols, bool vec)
 {
     Eight<T> v;
     if (vec && c + 8 <= cols) {
@@ -67,6 +67,13 @@ __device__ __forceinline__ void to_floats(const Eight<__half> &e, float (&v)[8])
     }
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
+{
+    uint32_t m;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+}
+
 // The largest magnitude of the eight values and `most`, as the bits of the type
 // with the sign cleared: ordered like the magnitudes, infinities and NaN above
 // every finite value.  16-bit types keep two maxima in one word.
@@ -75,13 +82,13 @@ __device__ __forceinline__ uint32_t most_of(const Eight<T> &e, uint32_t most)
 {
 #pragma unroll
     for (int i = 0; i < (int)sizeof(e.w) / 4; ++i)
-        most = sizeof(T) == 4 ? max(most, e.w[i] & 0x7fffffffu) : __vmaxu2(most, e.w[i] & 0x7fff7fffu);
+        most = sizeof(T) == 4 ? max(most, e.w[i] & 0x7fffffffu) : max_u16x2(most, e.w[i] & 0x7fff7fffu);
     return most;
 }
 template <typename T>
 __device__ __forceinline__ uint32_t most2(uint32_t a, uint32_t b)
 {
-    return sizeof(T) == 4 ? max(a, b) : __vmaxu2(a, b);
+    return sizeof(T) == 4 ? max(a, b) : max_u16x2(a, b);
 }
 // The maximum as a number (infinite or NaN if any value is).
 template <typename T>
@@ -106,7 +113,7 @@ __device__ __forceinline__ float step_of(float most)
 
 // rs: 1 / s correctly rounded.
 template <typename T>
-__device__ __forceinline__ void store8(uint8_t *row, int64_t c, int64_t cols, const Eight<T> &e, float s, float rs)
+__device__ __forceinline__ void store8(uint8_t *row, int c, int cols, const Eight<T> &e, float s, float rs)
 {
     float v[8];
     to_floats(e, v);
@@ -142,20 +149,22 @@ constexpr int kStrip = 1024;
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a)
 {
-    const int64_t kblocks = (a.cols + 127) / 128, strips = (a.cols + kStrip - 1) / kStrip;
+    // (columns fit 32 bits: at most 2^30)
+    const int cols = (int)a.cols, kblocks = (cols + 127) / 128, strips = (cols + kStrip - 1) / kStrip;
     const int lane = threadIdx.x & 31, sub = lane & 15;
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (row >= a.batch * a.rows) return;
     const int64_t e = a.batch > 1 ? row / a.rows : 0, r = row - e * a.rows;
     const T *src = (const T *)a.x + e * a.x_batch_stride + r * a.x_row_stride;
     uint8_t *dst = a.q + row * a.q_row_stride;
+    float *steps = a.steps + row * kblocks;
     const bool vec = ((uintptr_t)src & 15) == 0;
     bool finite = true;
-    for (int64_t strip = blockIdx.y; strip < strips; strip += gridDim.y) {
+    for (int strip = blockIdx.y; strip < strips; strip += gridDim.y) {
         Eight<T> v[4];
         uint32_t most[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = load8(src, strip * kStrip + i * 256 + lane * 8, a.cols, vec);
+        for (int i = 0; i < 4; ++i) v[i] = load8(src, strip * kStrip + i * 256 + lane * 8, cols, vec);
 #pragma unroll
         for (int i = 0; i < 4; ++i) most[i] = most_of(v[i], 0u);
 #pragma unroll
@@ -171,10 +180,10 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a)
         for (int i = 0; i < 4; ++i) {
             const float s = __shfl_sync(0xffffffffu, s_own, (lane & 16) | i);
             const float rs = __shfl_sync(0xffffffffu, rs_own, (lane & 16) | i);
-            const int64_t kb = strip * (kStrip / 128) + i * 2 + (lane >> 4);
+            const int kb = strip * (kStrip / 128) + i * 2 + (lane >> 4);
             if (kb < kblocks) {
-                store8(dst, kb * 128 + sub * 8, a.cols, v[i], s, rs);
-                if (sub == 0) a.steps[row * kblocks + kb] = s;
+                store8(dst, kb * 128 + sub * 8, cols, v[i], s, rs);
+                if (sub == 0) steps[kb] = s;
             }
         }
     }
@@ -193,13 +202,13 @@ __global__ void __launch_bounds__(kTileThreads, 2) quantize_tiles_kernel(const Q
     const int sub = threadIdx.x & 15, r0 = threadIdx.x >> 4;
     const T *src = (const T *)a.x + e * a.x_batch_stride;
     const bool vec = (((uintptr_t)src | (uintptr_t)(a.x_row_stride * (int64_t)sizeof(T))) & 15) == 0;
-    const int64_t c = (int64_t)kb * 128 + sub * 8;
+    const int c = (int)(kb * 128 + sub * 8);
     Eight<T> v[kTileLoads];
     uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < kTileLoads; ++i) {
         const int64_t r = (int64_t)rb * 128 + r0 + kTileRows * i;
-        v[i] = load8(src + r * a.x_row_stride, c, r < a.rows ? a.cols : 0, vec);
+        v[i] = load8(src + r * a.x_row_stride, c, r < a.rows ? (int)a.cols : 0, vec);
     }
 #pragma unroll
     for (int i = 0; i < kTileLoads; ++i) most = most_of(v[i], most);
@@ -215,7 +224,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) quantize_tiles_kernel(const Q
 #pragma unroll
     for (int i = 0; i < kTileLoads; ++i) {
         const int64_t r = (int64_t)rb * 128 + r0 + kTileRows * i;
-        if (r < a.rows) store8(a.q + ((int64_t)e * a.rows + r) * a.q_row_stride, c, a.cols, v[i], s, rs);
+        if (r < a.rows) store8(a.q + ((int64_t)e * a.rows + r) * a.q_row_stride, c, (int)a.cols, v[i], s, rs);
     }
     if (threadIdx.x == 0) a.steps[(int64_t)eb * kblocks + kb] = s;
 }
