@@ -42,7 +42,9 @@ enum Variant {
     kRowsDx256, kRowsDx64,      // dx = dy w
     kOuter,                     // dw = dy^T x
     kGramOne, kGramThree,       // X^T X from 16-bit samples / from three bf16 parts of fp32
-    kEightA256, kEightB64       // 8-bit operands: packed rows on D's rows / columns
+    kEightPair256, kEightPair128, kEightOne128,  // 8-bit operands, packed rows on D's rows: 256 of them
+                                                 // (a CTA pair) or 128, by 256 or 128 columns
+    kEightB64                                    // packed rows on D's columns
 };
 
 cudaError_t configure_rows();

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "common.cuh"
@@ -129,6 +130,39 @@ int split_of(int64_t tiles, int64_t stages, int64_t rows, int sms)
     return s;
 }
 
+// Tile of an 8-bit product with the packed rows on D's rows, and the CTAs that
+// share a tile's contraction: whichever needs the least time in whole rounds of
+// tiles over the SMs, at the clocks measured per 128-long step of the
+// contraction (8192 x 14336 x 4096) and for a join of parts.  Half of a group's
+// last tile is empty on average.
+Variant eight_variant(int64_t rows, int64_t n, int64_t k, int64_t experts, int sms, int &split)
+{
+    struct Shape { Variant v; int64_t m, w, ctas; double clocks; };
+    const Shape shapes[] = {{kEightPair256, 256, 256, 2, 1000}, {kEightPair128, 256, 128, 2, 600},
+                            {kEightOne128, 128, 128, 1, 630}};
+    const double join = 2500;
+    const int64_t steps = ceil64(k, 128);
+    Variant best = kEightPair256;
+    double least = 1e300;
+    split = 1;
+    for (const Shape &s : shapes) {
+        const double row_tiles_mean = experts == 1 ? (double)ceil64(rows, s.m) : (double)rows / s.m + 0.5 * experts;
+        const double mean = row_tiles_mean * ceil64(n, s.w);
+        const int64_t most = row_tiles(rows, experts, s.m) * ceil64(n, s.w);
+        // (three parts of 64 KB fit the first CTA's ring)
+        for (int p = 1; p <= (s.ctas == 1 ? 4 : 1); p *= 2) {
+            if (p > 1 && (most * p > sms || steps < 2 * p)) break;
+            const double cost = ceil(mean * s.ctas * p / sms) * ceil64(steps, p) * s.clocks + (p > 1 ? join : 0);
+            if (cost < least) {
+                least = cost;
+                best = s.v;
+                split = p;
+            }
+        }
+    }
+    return best;
+}
+
 // y[t, :] = x[t, :] w_e^T (columns = false: contraction over w's columns) or
 // x[t, :] w_e (columns = true: over w's rows).
 bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t ldx, const void *w, int64_t ldw,
@@ -245,12 +279,15 @@ bakron_status_t bakron_matmul_blocks(const uint8_t *x_dev, int64_t x_row_stride,
         return BAKRON_ERR_ALIGNMENT;
     // Packed rows on the tile's columns (64 at a time) while the groups are
     // short, on its 128 rows beyond that.
-    const bool small = rows <= 64 * experts;
-    const int64_t tiles = small ? row_tiles(rows, experts, 64) * ceil64(n, 128)
-                                : row_tiles(rows, experts, 128) * ceil64(n, 256);
-    if (tiles > kMaxTiles) return BAKRON_ERR_INVALID_ARG;
+    const bool small = rows <= 32 * experts;
+    if ((small ? row_tiles(rows, experts, 64) : row_tiles(rows, experts, 128)) * ceil64(n, 128) > kMaxTiles)
+        return BAKRON_ERR_INVALID_ARG;
     int sms = 0;
     if (configure_device(sms) != cudaSuccess) return BAKRON_ERR_CUDA;
+    int split = 1;
+    const Variant v = small ? kEightB64 : eight_variant(rows, n, k, experts, sms, split);
+    const int64_t m = small ? 64 : v == kEightOne128 ? 128 : 256, bn = v == kEightPair256 ? 256 : 128;
+    const int64_t tiles = row_tiles(rows, experts, m) * ceil64(n, bn);
     Args g{};
     if ((s = begin(ws_dev, ws_bytes, kStatusBytes, !rows, (cudaStream_t)stream, g)) != BAKRON_OK) return s;
     if (!rows) return BAKRON_OK;
@@ -267,15 +304,16 @@ bakron_status_t bakron_matmul_blocks(const uint8_t *x_dev, int64_t x_row_stride,
     g.x_steps = x_scales_dev;
     g.w_steps = w_scales_dev;
     g.w_step_rows = w_scale_rows;
-    if (small) g.split = split_of(tiles, ceil64(k, 128), rows, sms);
-    Maps m;
+    g.split = small ? split_of(tiles, ceil64(k, 128), rows, sms) : split;
+    Maps maps;
     const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    CUtensorMap *xm = small ? &m.b : &m.a, *wm = small ? &m.a : &m.b;
+    CUtensorMap *xm = small ? &maps.b : &maps.a, *wm = small ? &maps.a : &maps.b;
     if (!map2(xm, t, 1, x_dev, k, rows, x_row_stride, 128, small ? 32 : 128) ||
-        (small && !map2(&m.b2, t, 1, x_dev, k, rows, x_row_stride, 128, 64)) ||
-        !map3(wm, t, 1, w_dev, k, n, w_row_stride, experts, w_expert_stride, 128, small ? 128 : 64))
+        (small && !map2(&maps.b2, t, 1, x_dev, k, rows, x_row_stride, 128, 64)) ||
+        !map3(wm, t, 1, w_dev, k, n, w_row_stride, experts, w_expert_stride, 128,
+              small ? 128 : v == kEightPair256 ? 64 : (uint32_t)(bn * 128 / m)))
         return BAKRON_ERR_CUDA;
-    if (launch_eight(small ? kEightB64 : kEightA256, m, g, tiles, sms, (cudaStream_t)stream) !=
+    if (launch_eight(v, maps, g, tiles, sms, (cudaStream_t)stream) !=
         cudaSuccess)
         return BAKRON_ERR_CUDA;
     return BAKRON_OK;

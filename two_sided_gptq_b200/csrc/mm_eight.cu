@@ -10,10 +10,11 @@ namespace bakron {
 namespace mm {
 
 namespace {
+template <bool Pair, int BN>
 struct EightA {
     static constexpr Ragged kRagged = kTokensA;
-    static constexpr bool kPair = true, kEight = true, kAColumns = false, kLower = false;
-    static constexpr int kBN = 256, kPlanes = 1, kKRows = 0, kBoxRows = 128;
+    static constexpr bool kPair = Pair, kEight = true, kAColumns = false, kLower = false;
+    static constexpr int kBN = BN, kPlanes = 1, kKRows = 0, kBoxRows = 0;
 };
 struct EightB {
     static constexpr Ragged kRagged = kTokensB;
@@ -24,14 +25,21 @@ struct EightB {
 
 cudaError_t configure_eight()
 {
-    cudaError_t e = configure<EightA>();
+    cudaError_t e = configure<EightA<true, 256>>();
+    if (e == cudaSuccess) e = configure<EightA<true, 128>>();
+    if (e == cudaSuccess) e = configure<EightA<false, 128>>();
     return e == cudaSuccess ? configure<EightB>() : e;
 }
 
 cudaError_t launch_eight(Variant v, const Maps &maps, const Args &g, int64_t tiles, int sms,
                         cudaStream_t stream)
 {
-    return v == kEightA256 ? launch<EightA>(maps, g, tiles, sms, stream) : launch<EightB>(maps, g, tiles, sms, stream);
+    switch (v) {
+    case kEightPair256: return launch<EightA<true, 256>>(maps, g, tiles, sms, stream);
+    case kEightPair128: return launch<EightA<true, 128>>(maps, g, tiles, sms, stream);
+    case kEightOne128: return launch<EightA<false, 128>>(maps, g, tiles, sms, stream);
+    default: return launch<EightB>(maps, g, tiles, sms, stream);
+    }
 }
 
 }  // namespace mm

@@ -70,18 +70,23 @@ struct Shape {
     // a warp's staged steps: two chunks of its columns' (kTokensB), or one of them
     static constexpr int kStepFloats = P::kRagged == kTokensB ? 2 * kCols : kCols;
     // tiles whose contraction a cluster may split (few tiles, one per cluster)
-    static constexpr bool kSplit = P::kRagged == kTokensB && !P::kPair;
+    static constexpr bool kSplit = P::kRagged != kContract && !P::kPair;
     static constexpr int kRing = 227 * 1024 - kReserve - kTurnSpace;
     static constexpr int kStages = kRing / kStageBytes < 8 ? kRing / kStageBytes : 8;
     static constexpr int kAcc = P::kPlanes > 1 ? 2 : 1;             // accumulators per buffer
-    static constexpr int kTmemCols = 2 * kAcc * P::kBN;
-    // 8-bit chunks are short (one stage): the tile's two column halves are
+    // accumulator buffers: two, or as many as tensor memory holds where a chunk
+    // is one stage, so that the round trip MMA - epilogue - MMA (about 1000
+    // clocks, whatever the tile) is shared by several chunks
+    static constexpr int kBufs = P::kEight ? (P::kBN == 256 ? 2 : 4) : 2;
+    static constexpr int kTmemCols = kBufs * kAcc * P::kBN;
+    // with only two of them and short chunks the tile's two column halves are
     // separate MMAs with separate barriers, so that each is read out while the
     // other is computed
-    static constexpr int kHalves = P::kEight && P::kRagged == kTokensA ? 2 : 1;
+    static constexpr int kHalves = P::kEight && P::kBN == 256 ? 2 : 1;
     static constexpr int kThreads = 128 + 32 * kEpiWarps;
     // registers: the epilogue's accumulators and two loads in flight need more
     // than a 12-warp CTA's even share (168), the other warps far less
+    static constexpr bool kRowSteps = P::kEight && P::kRagged == kTokensA;  // a step per lane and chunk
     static constexpr bool kSplitRegs = kCols > 64;
     static constexpr int kRegsOthers = 56, kRegsEpilogue = 224;
     // a warpgroup can only take registers that the block was launched with
@@ -133,6 +138,16 @@ __device__ __forceinline__ int tiles_of_group(const Args &g, int len)
     return ceil_div(g.a_total, kM) * ceil_div(g.b_total, P::kBN);
 }
 
+// Tile i of rows x cols ones, in bands of eight rows, down each band's columns:
+// the tiles of one round over the SMs then form a block about as high as it is
+// wide, which reads the fewest operand bytes.
+__device__ __forceinline__ void raster(int i, int rows, int cols, int &row, int &col)
+{
+    const int band = i / (8 * cols), high = min(8, rows - 8 * band), in_band = i - band * 8 * cols;
+    row = 8 * band + in_band % high;
+    col = in_band / high;
+}
+
 template <class P>
 __device__ __forceinline__ Tile find_tile(const Args &g, const int *first, const uint16_t *order, int t)
 {
@@ -150,17 +165,19 @@ __device__ __forceinline__ Tile find_tile(const Args &g, const int *first, const
     int i = t - first[a];
     x.count = hi - lo;
     if (P::kRagged == kTokensB) {
-        const int mt = ceil_div(g.a_total, kM);
-        x.a0 = (i % mt) * kM;
-        x.b0 = lo + (i / mt) * P::kBN;
+        int row, col;
+        raster(i, ceil_div(g.a_total, kM), ceil_div(hi - lo, P::kBN), row, col);
+        x.a0 = row * kM;
+        x.b0 = lo + col * P::kBN;
         x.na = min(kM, g.a_total - x.a0);
         x.nb = min(P::kBN, hi - x.b0);
         x.k0 = 0;
         x.k1 = g.k_total;
     } else if (P::kRagged == kTokensA) {
-        const int mt = ceil_div(hi - lo, kM);
-        x.a0 = lo + (i % mt) * kM;
-        x.b0 = (i / mt) * P::kBN;
+        int row, col;
+        raster(i, ceil_div(hi - lo, kM), ceil_div(g.b_total, P::kBN), row, col);
+        x.a0 = lo + row * kM;
+        x.b0 = col * P::kBN;
         x.na = min(kM, hi - x.a0);
         x.nb = min(P::kBN, g.b_total - x.b0);
         x.k0 = 0;
@@ -216,12 +233,12 @@ __device__ __forceinline__ uint32_t word_of<__half>(float lo, float hi)
 }
 
 // Store this thread's accumulators: D row `lane_row` of the tile, columns
-// [col0, col0 + 2 N).
+// [col0, col0 + N).
 template <class P, typename T, int N>
 __device__ __forceinline__ void store_tile(const Args &g, const Tile &x, int lane_row, int col0,
-                                           const uint64_t (&acc)[N])
+                                           const float (&acc)[N])
 {
-    constexpr int C = 2 * N;
+    constexpr int C = N;
     T *out = (T *)g.out;
     if (lane_row >= x.na) return;
     if (P::kRagged == kTokensB) {
@@ -233,14 +250,14 @@ __device__ __forceinline__ void store_tile(const Args &g, const Tile &x, int lan
 #pragma unroll
         for (int c = 0; c < C; ++c)
             if (col0 + c < x.nb) {
-                const float v = element(acc, c);
+                const float v = acc[c];
                 p[(int64_t)c * g.ldo] = round_to<T>(P::kEight ? v * s : v);
             }
     } else {
         T *p = out + (P::kRagged == kContract ? (int64_t)x.e * g.out_expert_stride : 0) +
                (int64_t)(x.a0 + lane_row) * g.ldo + x.b0 + col0;
         const int n = min(C, x.nb - col0);
-        auto value = [&](int c) { return element(acc, c); };
+        auto value = [&](int c) { return acc[c]; };
         if (n == C && ((uintptr_t)p & 31) == 0) {
             // one whole 32-byte sector per store
             constexpr int kVec = 32 / sizeof(T);
@@ -270,10 +287,10 @@ constexpr int kTurnRows = 32;
 constexpr int kTurnBytes = kTurnRows * kBM * 2;
 template <class P, typename T, int N>
 __device__ __forceinline__ void store_turned(const Args &g, const Tile &x, int rank, int thread, int half,
-                                             const uint64_t (&acc)[N], T *buf)
+                                             const float (&acc)[N], T *buf)
 {
     const int row0 = rank * kBM;                 // this CTA's first D row
-    const int col0 = half * 2 * N;
+    const int col0 = half * N;
     float s = 1.f;
     if (P::kEight && g.w_step_rows == 1 && row0 + thread < x.na)
         s = __ldg(g.w_steps + (int64_t)x.e * g.a_total + x.a0 + row0 + thread);
@@ -281,12 +298,12 @@ __device__ __forceinline__ void store_turned(const Args &g, const Tile &x, int r
     const int valid = x.na - row0 - piece;
     T *out = (T *)g.out + (int64_t)(x.b0 + col0) * g.ldo + x.a0 + row0 + piece;
 #pragma unroll
-    for (int c0 = 0; c0 < 2 * N; c0 += kTurnRows) {
+    for (int c0 = 0; c0 < N; c0 += kTurnRows) {
         if (col0 + c0 >= x.nb) break;
         asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
 #pragma unroll
         for (int c = 0; c < kTurnRows; ++c) {
-            const float v = element(acc, c0 + c);
+            const float v = acc[c0 + c];
             buf[c * kBM + thread] = round_to<T>(P::kEight ? v * s : v);
         }
         asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
@@ -313,21 +330,21 @@ __device__ __forceinline__ void store_turned(const Args &g, const Tile &x, int r
 // and their mirror images.
 template <int N>
 __device__ __forceinline__ void store_gram(const Args &g, const Tile &x, int lane_row, int col0,
-                                           const uint64_t (&acc)[N])
+                                           const float (&acc)[N])
 {
     if (lane_row >= x.na) return;
     const int64_t d = g.ldo;
     float *out = (float *)g.out + (int64_t)x.e * g.out_expert_stride;
     const int i = x.a0 + lane_row, j0 = x.b0 + col0;
     const float count = (float)max(x.count, 1), rcount = __frcp_rn(count);
-    auto value = [&](int c) { return div_rn_recip(element(acc, c), count, rcount); };
+    auto value = [&](int c) { return div_rn_recip(acc[c], count, rcount); };
     float *row = out + i * d + j0, *col = out + j0 * d + i;
     const bool vec = ((uintptr_t)row & 31) == 0;
     // Eight columns at a time: whole 32-byte sectors along the row where all
     // eight are below the diagonal, and a warp's 32 rows next to each other in
     // the mirror image.
 #pragma unroll
-    for (int c = 0; c < 2 * N; c += 8) {
+    for (int c = 0; c < N; c += 8) {
         const int n = min(x.nb - col0, i + 1 - j0) - c;  // columns of these that are written
         if (n >= 8 && vec) {
             uint32_t v[8];
@@ -408,10 +425,13 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     auto empty_bar = [&](int s) { return bar0 + 8u * (S::kStages + s); };
     auto tail_full_bar = [&](int s) { return bar0 + 8u * (2 * S::kStages + s); };  // a tail stage has landed in this CTA
     auto tail_done_bar = [&](int s) { return bar0 + 8u * (3 * S::kStages + s); };  // the CTAs have zeroed their tails
-    auto accf_bar = [&](int b, int h) { return bar0 + 8u * (4 * S::kStages + 2 * h + b); };
-    auto acce_bar = [&](int b, int h) { return bar0 + 8u * (4 * S::kStages + 4 + 2 * h + b); };
-    const uint32_t drain_bar = bar0 + 8u * (4 * S::kStages + 8);
-    static_assert(4 * S::kStages + 9 <= 48, "barriers");
+    auto accf_bar = [&](int b, int h) { return bar0 + 8u * (4 * S::kStages + S::kBufs * h + b); };
+    auto acce_bar = [&](int b, int h) { return bar0 + 8u * (4 * S::kStages + S::kBufs * (S::kHalves + h) + b); };
+    const uint32_t drain_bar = bar0 + 8u * (4 * S::kStages + 2 * S::kBufs * S::kHalves);
+    static_assert(4 * S::kStages + 2 * S::kBufs * S::kHalves + 1 <= 48, "barriers");
+    // accumulator chunk number c: its buffer and the parity of its buffer's use
+    auto buf_of = [](int c) { return c % S::kBufs; };
+    auto use_of = [](int c) { return c / S::kBufs & 1; };
 
     if (threadIdx.x == 0) {
         prefetch_map(&maps.a);
@@ -422,7 +442,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             mbar_init(tail_full_bar(s), 1);
             mbar_init(tail_done_bar(s), S::kCtas);
         }
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < S::kBufs; ++b)
             for (int h = 0; h < S::kHalves; ++h) {
                 mbar_init(accf_bar(b, h), 1);
                 mbar_init(acce_bar(b, h), S::kEpiWarps * S::kCtas / S::kHalves);
@@ -653,10 +673,10 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                 const uint32_t idesc = g.idesc | ((uint32_t)(n_mma >> 3) << 17) | ((uint32_t)(S::kM >> 4) << 24);
                 const int kb0 = stage_begin(nkb), kb1 = stage_end(nkb);
                 for (int kb = kb0, in_chunk = 0; kb < kb1; ++kb, ++it) {
-                    const int buf = chunk & 1;
+                    const int buf = buf_of(chunk);
                     const int s = it % S::kStages;
-                    if (S::kHalves == 1 && in_chunk == 0 && chunk >= 2)
-                        ok = wait(acce_bar(buf, 0), ((chunk >> 1) - 1) & 1);
+                    if (S::kHalves == 1 && in_chunk == 0 && chunk >= S::kBufs)
+                        ok = wait(acce_bar(buf, 0), use_of(chunk) ^ 1);
                     ok = ok && wait(full_bar(s), (it / S::kStages) & 1);
                     int steps = kSteps;
                     if (P::kRagged == kContract) {
@@ -678,7 +698,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                     if constexpr (S::kHalves > 1) {
 #pragma unroll
                         for (int h = 0; h < S::kHalves; ++h) {
-                            ok = ok && (chunk < 2 || wait(acce_bar(buf, h), ((chunk >> 1) - 1) & 1));
+                            ok = ok && (chunk < S::kBufs || wait(acce_bar(buf, h), use_of(chunk) ^ 1));
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
@@ -765,9 +785,9 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             const int nchunk = ceil_div(stage_end(nkb) - kb0, chunk_stages);
             // 16-column loads of each chunk: the tile's valid columns only
             const int loads = min(max(ceil_div(x.nb - col0, 16), 0), S::kCols / 16) * S::kAcc;
-            uint64_t acc[S::kCols / 2];  // packed pairs of FP32 columns
+            float acc[S::kCols];
 #pragma unroll
-            for (int i = 0; i < S::kCols / 2; ++i) acc[i] = 0;
+            for (int i = 0; i < S::kCols; ++i) acc[i] = 0.f;
             // 8-bit operands: the steps of this thread's share of the tile
             const float *xs = nullptr, *ws = nullptr;
             bool own_row = false;
@@ -783,53 +803,23 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                                       min((x.a0 + rank * kBM) / 128, ceil_div(g.a_total, 128) - 1)) * nkb;
                 }
             }
-            // (kTokensA: the row's steps are fetched four chunks at a time, the
-            // weight's one, a chunk or more ahead of their use)
-            float4 xs_now = make_float4(0, 0, 0, 0), xs_next = xs_now;
-            float ws_next = ws ? __ldg(ws) : 1.f;
-            const bool xs_vec = (nkb & 3) == 0;  // the row's steps start on a 16-byte boundary
-            auto four_steps = [&](int c) {
-                if (xs_vec) return __ldg((const float4 *)(xs + c));
-                return make_float4(__ldg(xs + c), c + 1 < nkb ? __ldg(xs + c + 1) : 0.f,
-                                   c + 2 < nkb ? __ldg(xs + c + 2) : 0.f, c + 3 < nkb ? __ldg(xs + c + 3) : 0.f);
-            };
-            if (own_row) xs_next = four_steps(0);
             const int bar_half = S::kHalves > 1 ? half : 0;
-            for (int c = 0; c < nchunk; ++c, ++chunk) {
-                const int buf = chunk & 1;
-                uint64_t row_step = 0;
-                if (P::kEight && P::kRagged == kTokensA) {
-                    if ((c & 3) == 0) {
-                        xs_now = xs_next;
-                        if (own_row && c + 4 < nchunk) xs_next = four_steps(c + 4);
-                    }
-                    const float s = xs_now.x * ws_next;
-                    row_step = pack2(s, s);
-                    xs_now.x = xs_now.y;
-                    xs_now.y = xs_now.z;
-                    xs_now.z = xs_now.w;
-                    if (ws && c + 1 < nchunk) ws_next = __ldg(ws + c + 1);
-                }
-                float *steps = steps_w + (c & 1) * S::kCols;
-                if (P::kEight && P::kRagged == kTokensB) {
-                    const float s = ws ? __ldg(ws + kb0 + c) : 1.f;
-                    for (int j = lane; j < S::kCols; j += 32)
-                        steps[j] = col0 + j < x.nb ? __ldg(g.x_steps + (int64_t)(x.b0 + col0 + j) * nkb + kb0 + c) * s : 0.f;
-                    __syncwarp();
-                }
-                ok = __all_sync(0xffffffffu, wait(accf_bar(buf, bar_half), (chunk >> 1) & 1));
-                if (!ok) break;
+            // One chunk: wait for it, add it, give its buffer back.
+            auto take = [&](float row_step, const float *steps) {
+                const int buf = buf_of(chunk);
+                ok = wait(accf_bar(buf, bar_half), use_of(chunk)) && ok;
+                __syncwarp();
                 tc_fence_after();
                 const uint32_t src = tmem_base + lane_off + (uint32_t)(buf * S::kAcc * BN + col0);
                 auto addr = [&](int l) { return src + (uint32_t)((l / S::kAcc) * 16 + (l % S::kAcc) * BN); };
                 auto add = [&](const uint32_t (&r)[16], int l) {
-                    const int c0 = (l / S::kAcc) * 8;
+                    const int c0 = (l / S::kAcc) * 16;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint64_t v = pack2(r[2 * i], r[2 * i + 1]);
-                        if (P::kEight && P::kRagged == kTokensA) fma2(acc[c0 + i], v, row_step);
-                        else if (P::kEight) fma2(acc[c0 + i], v, *(const uint64_t *)(steps + 2 * (c0 + i)));
-                        else add2(acc[c0 + i], v);
+                    for (int i = 0; i < 16; ++i) {
+                        const float v = __uint_as_float(r[i]);
+                        if (S::kRowSteps) acc[c0 + i] = fmaf(v, row_step, acc[c0 + i]);
+                        else if (P::kEight) acc[c0 + i] = fmaf(v, steps[c0 + i], acc[c0 + i]);
+                        else acc[c0 + i] += v;
                     }
                 };
                 constexpr int kLoads = S::kCols / 16 * S::kAcc;
@@ -838,7 +828,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        const uint32_t bar = first_cta_acce + 8u * (2 * bar_half + buf);
+                        const uint32_t bar = first_cta_acce + 8u * (S::kBufs * bar_half + buf);
                         if (kPair) mbar_arrive_remote(bar);
                         else mbar_arrive(bar);
                     }
@@ -867,6 +857,44 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                         }
                     release();
                 }
+                ++chunk;
+            };
+            if constexpr (S::kRowSteps) {
+                // the row's and the weight's steps four chunks at a time, fetched
+                // four chunks ahead
+                const bool vec = ((nkb | kb0) & 3) == 0;  // both start on 16-byte boundaries
+                auto four = [&](const float *p, int c) {
+                    if (vec) return __ldg((const float4 *)(p + c));
+                    return make_float4(__ldg(p + c), c + 1 < nkb ? __ldg(p + c + 1) : 0.f,
+                                       c + 2 < nkb ? __ldg(p + c + 2) : 0.f, c + 3 < nkb ? __ldg(p + c + 3) : 0.f);
+                };
+                float4 xn = make_float4(0, 0, 0, 0), wn = make_float4(1, 1, 1, 1);
+                if (own_row) xn = four(xs, kb0);
+                if (ws) wn = four(ws, kb0);
+                for (int c = 0; c < nchunk && ok; c += 4) {
+                    const float s[4] = {xn.x * wn.x, xn.y * wn.y, xn.z * wn.z, xn.w * wn.w};
+                    if (c + 4 < nchunk) {
+                        if (own_row) xn = four(xs, kb0 + c + 4);
+                        if (ws) wn = four(ws, kb0 + c + 4);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c + i < nchunk) take(s[i], nullptr);
+                    ok = __all_sync(0xffffffffu, ok);
+                }
+            } else {
+                for (int c = 0; c < nchunk && ok; ++c) {
+                    float *steps = steps_w + (c & 1) * S::kCols;
+                    if (P::kEight) {
+                        const float s = ws ? __ldg(ws + kb0 + c) : 1.f;
+                        for (int j = lane; j < S::kCols; j += 32)
+                            steps[j] =
+                                col0 + j < x.nb ? __ldg(g.x_steps + (int64_t)(x.b0 + col0 + j) * nkb + kb0 + c) * s : 0.f;
+                        __syncwarp();
+                    }
+                    take(0.f, steps);
+                    ok = __all_sync(0xffffffffu, ok);
+                }
             }
             if constexpr (S::kSplit) {
                 if (split > 1) {
@@ -879,7 +907,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                         const uint32_t dst = map_rank(smem_u32(slot + (part - 1) * part_floats), 0);
 #pragma unroll
                         for (int c = 0; c < S::kCols; ++c)
-                            if (c < 16 * loads) store_cluster(dst + c * (kBM * 4), element(acc, c));
+                            if (c < 16 * loads) store_cluster(dst + c * (kBM * 4), acc[c]);
                     }
                     cluster_sync();
                     joined = true;
@@ -887,8 +915,8 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                     for (int p = 0; p < split - 1; ++p) {
                         const float *from = slot + p * part_floats;
 #pragma unroll
-                        for (int c = 0; c < S::kCols; c += 2)
-                            if (c < 16 * loads) add2(acc[c / 2], pack2(from[c * kBM], from[(c + 1) * kBM]));
+                        for (int c = 0; c < S::kCols; ++c)
+                            if (c < 16 * loads) acc[c] += from[c * kBM];
                     }
                 }
             }
@@ -900,7 +928,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                 for (int j = lane; j < S::kCols; j += 32) steps_w[j] = col0 + j < x.nb ? __ldg(s + j) : 0.f;
                 __syncwarp();
 #pragma unroll
-                for (int c = 0; c < S::kCols / 2; ++c) mul2(acc[c], *(const uint64_t *)(steps_w + 2 * c));
+                for (int c = 0; c < S::kCols; ++c) acc[c] *= steps_w[c];
             }
             if constexpr (P::kLower) {
                 store_gram(g, x, lane_row, col0, acc);
