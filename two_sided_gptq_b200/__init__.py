@@ -328,27 +328,20 @@ def gram(X, damping=0.0, *, ws=None, out=None, stream=None, check_status=True):
 # ------------------------------------------------- products over packed rows
 STATUS_BYTES = 256  # workspace of the calls below that need no more than the status block
 
-_type_ids = None
-
-
-def _types():
-    """torch dtype -> bakron_type_t."""
-    global _type_ids
-    if _type_ids is None:
-        torch = _torch()
-        _type_ids = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    return _type_ids
-
-
-_raw_module = None
+# set by the first _device(): torch dtype -> bakron_type_t, the types that the
+# calls take, torch's binding module
+_type_ids = _eight = _single = _half = _bytes = _offset = _raw_module = None
 
 
 def _device():
     """The current device's index (asked once per call, through torch's binding
     module: the checks of a small product would otherwise cost more than it)."""
-    global _raw_module
+    global _type_ids, _eight, _single, _half, _bytes, _offset, _raw_module
     if _raw_module is None:
         torch = _torch()
+        _type_ids = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+        _eight, _single, _half = (torch.float8_e4m3fn,), (torch.float32,), (torch.bfloat16, torch.float16)
+        _bytes, _offset = torch.uint8, (torch.int32,)
         if not torch.cuda.is_available():
             return None  # no tensor is on it
         _raw_module = torch._C
@@ -358,8 +351,9 @@ def _device():
 def _here(t, name, dims, dtypes, dev):
     """A CUDA tensor on device ``dev`` with unit stride along its last dimension."""
     try:
-        if (t.dtype in dtypes and t.dim() in dims and t.get_device() == dev
-                and (t.stride(-1) == 1 or t.shape[-1] <= 1)):
+        stride = t.stride()
+        if (t.dtype in dtypes and len(stride) in dims and t.get_device() == dev
+                and (stride[-1] == 1 or t.shape[-1] <= 1)):
             return
     except AttributeError:
         pass
@@ -378,7 +372,7 @@ def _ld(t, dim, least, align):
 
 
 def _groups(offsets, dev, experts=None):
-    _here(offsets, "offsets", (1,), (_torch().int32,), dev)
+    _here(offsets, "offsets", (1,), _offset, dev)
     n = offsets.shape[0]
     if n < 2 or (experts is not None and n != experts + 1):
         raise ValueError("offsets must hold one bound more than there are experts")
@@ -402,9 +396,9 @@ def _call(name, args, ws, stream, check_status, dev, need=STATUS_BYTES):
     """One library call on a workspace: ``ws``, or a new one."""
     if ws is None:
         ws = workspace(need, dev)
-    elif ws.get_device() != dev or ws.dtype != _torch().uint8 or not ws.is_contiguous():
+    elif ws.get_device() != dev or ws.dtype != _bytes or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous uint8 tensor on the current device")
-    lib, at, size = _lib(), ws.data_ptr(), ws.numel()
+    lib, at, size = _native._lib or _lib(), ws.data_ptr(), ws.numel()
     st = _raw_module._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     status = getattr(lib, name)(*args, at, size, st)
     if status:
@@ -425,7 +419,7 @@ def quantize_blocks(x, block_rows=1, *, out=None, ws=None, stream=None, check_st
     block_rows), ceil(cols / 128)]``.  ``out`` may supply both."""
     torch = _torch()
     dev = _device()
-    _here(x, "x", (2, 3), _types(), dev)
+    _here(x, "x", (2, 3), _type_ids, dev)
     rows, cols = x.shape[-2:]
     batch = x.shape[0] if x.dim() == 3 else 1
     lead = tuple(x.shape[:-2])
@@ -446,7 +440,7 @@ def quantize_blocks(x, block_rows=1, *, out=None, ws=None, stream=None, check_st
         raise ValueError("codes must hold its matrices one directly after another")
     ldx = _ld(x, -2, cols, 1)
     _call("bakron_quantize_blocks",
-          (x.data_ptr(), _types()[x.dtype], batch, rows, cols, x.stride(0) if batch > 1 else 0, ldx, block_rows,
+          (x.data_ptr(), _type_ids[x.dtype], batch, rows, cols, x.stride(0) if batch > 1 else 0, ldx, block_rows,
            q.data_ptr(), ldq, scales.data_ptr()), ws, stream, check_status, dev)
     return q, scales
 
@@ -466,39 +460,43 @@ def matmul_blocks(x, x_scales, w, w_scales, offsets=None, *, out_dtype=None, out
     are multiplied by ``w[e]``; rows outside every group keep what ``out`` holds
     (unspecified in a new result).  Result: rows x n, bfloat16 unless
     ``out_dtype`` or ``out`` says float16 or float32."""
-    torch = _torch()
-    f8, f32 = (torch.float8_e4m3fn,), (torch.float32,)
     dev = _device()
     lead = 0 if offsets is None else 1
+    f8, f32 = _eight, _single
     _here(x, "x", (2,), f8, dev), _here(x_scales, "x_scales", (2,), f32, dev)
     _here(w, "w", (2 + lead,), f8, dev), _here(w_scales, "w_scales", (1 + lead, 2 + lead), f32, dev)
     rows, k = x.shape
-    n, kw = w.shape[-2:]
-    experts = _groups(offsets, dev, w.shape[0]) if lead else 1
-    kblocks = -(-k // 128)
-    per_row = w_scales.dim() == 1 + lead
-    steps = (n,) if per_row else (-(-n // 128), kblocks)
-    if kw != k or x_scales.shape != (rows, kblocks) or w_scales.shape != ((experts,) + steps if lead else steps):
+    kblocks = (k + 127) // 128
+    if lead:
+        experts, n, kw = w.shape
+        _groups(offsets, dev, experts)
+        stride, at = w.stride(), offsets.data_ptr()
+    else:
+        n, kw = w.shape
+        experts, stride, at = 1, (0,) + w.stride(), 0
+    given = w_scales.shape
+    per_row = len(given) == 1 + lead
+    if (kw != k or x_scales.shape != (rows, kblocks) or given[lead:] != ((n,) if per_row else ((n + 127) // 128, kblocks))
+            or (lead and given[0] != experts)):
         raise ValueError("x is rows x k with steps rows x ceil(k/128); w is n x k with steps ceil(n/128) x "
                          "ceil(k/128) or (n,), under one leading dimension when offsets are given")
     if not x_scales.is_contiguous() or not w_scales.is_contiguous():
         raise ValueError("x_scales and w_scales must be contiguous")
-    if out is None and out_dtype is None:
-        out_dtype = torch.bfloat16
-    y = _result(out, (rows, n), out_dtype, _types(), dev)
-    ldw = _ld(w, -2, k, 16)
+    types = _type_ids
+    y = _result(out, (rows, n), out_dtype if out is not None or out_dtype is not None else _torch().bfloat16, types, dev)
+    wide = (k + 15) // 16 * 16  # a stride that will do where there is one row
+    ldw = stride[1] if n > 1 else wide
     _call("bakron_matmul_blocks",
-          (x.data_ptr(), _ld(x, 0, k, 16), x_scales.data_ptr(), w.data_ptr(), ldw,
-           w.stride(0) if experts > 1 else -(-n * ldw // 16) * 16, w_scales.data_ptr(), 1 if per_row else 128,
-           offsets.data_ptr() if offsets is not None else 0, experts, y.data_ptr(), _types()[y.dtype],
-           _ld(y, 0, n, 1), rows, n, k), ws, stream, check_status, dev)
+          (x.data_ptr(), x.stride(0) if rows > 1 else wide, x_scales.data_ptr(), w.data_ptr(), ldw,
+           stride[0] if experts > 1 else (n * ldw + 15) // 16 * 16, w_scales.data_ptr(), 1 if per_row else 128, at,
+           experts, y.data_ptr(), types[y.dtype], y.stride(0) if rows > 1 else n, rows, n, k), ws, stream, check_status,
+          dev)
     return y
 
 
 def _grouped(name, x, w, offsets, across, out_dtype, out, ws, stream, check_status):
-    torch = _torch()
     dev = _device()
-    _here(x, "x" if across == 2 else "dy", (2,), (torch.bfloat16, torch.float16), dev)
+    _here(x, "x" if across == 2 else "dy", (2,), _half, dev)
     dtype = x.dtype
     _here(w, "w", (3,), (dtype,), dev)
     experts, n, k = w.shape
@@ -509,11 +507,11 @@ def _grouped(name, x, w, offsets, across, out_dtype, out, ws, stream, check_stat
     width = n if across == 2 else k
     if out is None and out_dtype is None:
         out_dtype = dtype
-    y = _result(out, (rows, width), out_dtype, (dtype, torch.float32), dev)
+    y = _result(out, (rows, width), out_dtype, (dtype,) + _single, dev)
     ldw = _ld(w, 1, k, 8)
-    _call(name, (x.data_ptr(), _types()[dtype], _ld(x, 0, into, 8), w.data_ptr(), ldw,
+    _call(name, (x.data_ptr(), _type_ids[dtype], _ld(x, 0, into, 8), w.data_ptr(), ldw,
                  w.stride(0) if experts > 1 else n * ldw, offsets.data_ptr(), experts, y.data_ptr(),
-                 _types()[y.dtype], _ld(y, 0, width, 1), rows, n, k), ws, stream, check_status, dev)
+                 _type_ids[y.dtype], _ld(y, 0, width, 1), rows, n, k), ws, stream, check_status, dev)
     return y
 
 
@@ -551,8 +549,8 @@ def matmul_grouped_dw(dy, x, offsets, *, out_dtype=None, out=None, ws=None, stre
     if not dw.is_contiguous():
         raise ValueError("out must be contiguous")
     _call("bakron_matmul_grouped_dw",
-          (dy.data_ptr(), _types()[x.dtype], _ld(dy, 0, n, 8), x.data_ptr(), _ld(x, 0, k, 8), offsets.data_ptr(),
-           experts, dw.data_ptr(), _types()[dw.dtype], rows, n, k), ws, stream, check_status, dev)
+          (dy.data_ptr(), _type_ids[x.dtype], _ld(dy, 0, n, 8), x.data_ptr(), _ld(x, 0, k, 8), offsets.data_ptr(),
+           experts, dw.data_ptr(), _type_ids[dw.dtype], rows, n, k), ws, stream, check_status, dev)
     return dw
 
 
@@ -564,13 +562,13 @@ def gram_grouped(X, offsets, damping=0.0, *, ws=None, out=None, stream=None, che
     without rows (``bakron_gram_grouped``)."""
     torch = _torch()
     dev = _device()
-    _here(X, "X", (2,), _types(), dev)
+    _here(X, "X", (2,), _type_ids, dev)
     experts = _groups(offsets, dev)
     rows, d = X.shape
     A = _result(out, (experts, d, d), torch.float32, (torch.float32,), dev)
     if not A.is_contiguous():
         raise ValueError("out must be contiguous")
-    t = _types()[X.dtype]
+    t = _type_ids[X.dtype]
     need = _lib().bakron_gram_grouped_workspace_size(t, rows, d) if ws is None else 0
     _call("bakron_gram_grouped", (X.data_ptr(), t, _ld(X, 0, d, 8), offsets.data_ptr(), experts, float(damping),
                                   A.data_ptr(), rows, d), ws, stream, check_status, dev, need)
