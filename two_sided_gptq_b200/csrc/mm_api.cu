@@ -120,13 +120,12 @@ int64_t row_tiles(int64_t rows, int64_t experts, int64_t tile)
 }
 
 // CTAs per tile of a call with short groups: while the tiles would leave half
-// the SMs idle the contraction is split, down to two stages a CTA, as long as
-// the other parts' sums fit the first CTA's ring (192 KB of it).
-int split_of(int64_t tiles, int64_t stages, int64_t rows, int sms)
+// the SMs idle the contraction is split, down to two stages a CTA (eight CTAs
+// are the most a cluster holds on every device).
+int split_of(int64_t tiles, int64_t stages, int sms)
 {
-    const int64_t part_bytes = ceil64(rows < 64 ? rows : 64, 16) * 16 * 128 * 4;
     int s = 1;
-    while (s < 8 && tiles * s * 2 <= sms && stages >= 4 * s && (2 * s - 1) * part_bytes <= 192 * 1024) s *= 2;
+    while (s < 8 && tiles * s * 2 <= sms && stages >= 4 * s) s *= 2;
     return s;
 }
 
@@ -140,7 +139,7 @@ Variant eight_variant(int64_t rows, int64_t n, int64_t k, int64_t experts, int s
     struct Shape { Variant v; int64_t m, w, ctas; double clocks; };
     const Shape shapes[] = {{kEightPair256, 256, 256, 2, 1000}, {kEightPair128, 256, 128, 2, 600},
                             {kEightOne128, 128, 128, 1, 630}};
-    const double join = 2500;
+    const double join = 1800;
     const int64_t steps = ceil64(k, 128);
     Variant best = kEightPair256;
     double least = 1e300;
@@ -149,8 +148,7 @@ Variant eight_variant(int64_t rows, int64_t n, int64_t k, int64_t experts, int s
         const double row_tiles_mean = experts == 1 ? (double)ceil64(rows, s.m) : (double)rows / s.m + 0.5 * experts;
         const double mean = row_tiles_mean * ceil64(n, s.w);
         const int64_t most = row_tiles(rows, experts, s.m) * ceil64(n, s.w);
-        // (three parts of 64 KB fit the first CTA's ring)
-        for (int p = 1; p <= (s.ctas == 1 ? 4 : 1); p *= 2) {
+        for (int p = 1; p <= (s.ctas == 1 ? 8 : 1); p *= 2) {
             if (p > 1 && (most * p > sms || steps < 2 * p)) break;
             const double cost = ceil(mean * s.ctas * p / sms) * ceil64(steps, p) * s.clocks + (p > 1 ? join : 0);
             if (cost < least) {
@@ -203,7 +201,7 @@ bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t 
     g.ldo = ldy;
     g.out_type = y_type;
     g.turn = y_type != BAKRON_F32 && ldy % 8 == 0;
-    if (small) g.split = split_of(tiles, ceil64(in, 64), rows, sms);
+    if (small) g.split = split_of(tiles, ceil64(in, 64), sms);
     g.idesc = idesc16(type, columns, false);
     g.chunk = y_type == BAKRON_F32 ? kChunkF32 : kChunk16;
     Maps m;
@@ -304,7 +302,7 @@ bakron_status_t bakron_matmul_blocks(const uint8_t *x_dev, int64_t x_row_stride,
     g.x_steps = x_scales_dev;
     g.w_steps = w_scales_dev;
     g.w_step_rows = w_scale_rows;
-    g.split = small ? split_of(tiles, ceil64(k, 128), rows, sms) : split;
+    g.split = small ? split_of(tiles, ceil64(k, 128), sms) : split;
     Maps maps;
     const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     CUtensorMap *xm = small ? &maps.b : &maps.a, *wm = small ? &maps.a : &maps.b;

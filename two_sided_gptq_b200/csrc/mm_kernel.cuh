@@ -465,10 +465,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         }
     }
-    // the next kernel's CTAs may start their own set-up; everything below may
-    // touch what earlier kernels wrote
-    pdl_trigger();
-    pdl_wait();
+    pdl_wait();  // everything below may touch what earlier kernels wrote
     if (warp == 2) {
         // tile numbering: exclusive prefix sum of the groups' tile counts;
         // where a tile's cost is its group's length, longest groups first
@@ -898,26 +895,33 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             }
             if constexpr (S::kSplit) {
                 if (split > 1) {
-                    // every part's MMAs have read their stages: the first CTA's
-                    // ring takes the other parts' sums, added in their order
-                    cluster_sync();
-                    float *slot = (float *)smem + quad * 32 + lane + (int64_t)col0 * kBM;
-                    const int part_floats = ((min(x.nb, BN) + 15) & ~15) * kBM;
+                    // This part's MMAs have read all its stages, so its ring can
+                    // take its sums; the first CTA reads the others' there, in
+                    // their order, and the others stay until it has.
+                    float *mine = (float *)smem + (int64_t)col0 * kBM + quad * 32 + lane;
                     if (part) {
-                        const uint32_t dst = map_rank(smem_u32(slot + (part - 1) * part_floats), 0);
 #pragma unroll
                         for (int c = 0; c < S::kCols; ++c)
-                            if (c < 16 * loads) store_cluster(dst + c * (kBM * 4), acc[c]);
+                            if (c < 16 * loads) mine[c * kBM] = acc[c];
                     }
                     cluster_sync();
+                    if (!part) {
+                        for (int p = 1; p < split; ++p) {
+                            const uint32_t from = map_rank(smem_u32(mine), p);
+#pragma unroll
+                            for (int c = 0; c < S::kCols; c += 16)
+                                if (c < 16 * loads) {
+                                    float v[16];  // sixteen loads in flight
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) v[i] = load_cluster(from + (c + i) * (kBM * 4));
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) acc[c + i] += v[i];
+                                }
+                        }
+                    }
+                    cluster_arrive();
                     joined = true;
                     if (part) break;
-                    for (int p = 0; p < split - 1; ++p) {
-                        const float *from = slot + p * part_floats;
-#pragma unroll
-                        for (int c = 0; c < S::kCols; ++c)
-                            if (c < 16 * loads) acc[c] += from[c * kBM];
-                    }
                 }
             }
             if (!ok) break;
@@ -952,11 +956,15 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     if constexpr (S::kSplit) {
         // warps that have not taken part in the join arrive at its barriers
         __syncwarp();
-        if (split > 1 && !joined) {
-            cluster_sync();
-            cluster_sync();
+        if (split > 1) {
+            if (!joined) {
+                cluster_sync();
+                cluster_arrive();
+            }
+            cluster_wait();
         }
     }
+    pdl_trigger();  // the next kernel's CTAs may start their own set-up
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0) report(g.st, error_sh);
