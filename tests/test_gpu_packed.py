@@ -206,6 +206,37 @@ def test_matmul_blocks_grouped(bk, lens, lead, tail, n, k, per_row):
             check_close(got[a:b].cpu(), want, size, k, 4, 128, f"expert {e}")
 
 
+@pytest.mark.parametrize("per_row", [False, True])
+@pytest.mark.parametrize("rows,n,k", [(1500, 5000, 300), (300, 4100, 520), (100, 130, 1100), (200, 260, 900),
+                                      (2100, 1030, 130), (50, 1000, 2000), (520, 3000, 1300)])
+def test_matmul_blocks_every_tile_shape(bk, rows, n, k, per_row):
+    """Sizes that reach the 256 x 256, 256 x 128 and 128 x 128 tiles, whole and
+    split along the contraction, with ragged edges and uneven parts."""
+    x, xs = eight(rows, k, rows + k)
+    w, ws = weights(n, k, per_row, n + k)
+    want, size = blocks_reference(x, xs, w, ws)
+    y = bk.matmul_blocks(rows8(x), xs.cuda(), rows8(w), ws.cuda(), out_dtype=F32)
+    check_close(y.cpu(), want, size, k, 4, 128, f"blocks {rows}x{n}x{k}")
+    y = bk.matmul_blocks(rows8(x), xs.cuda(), rows8(w), ws.cuda())
+    check_close(y.cpu(), want, size, k, 4, 128, f"blocks {rows}x{n}x{k} bf16")
+
+
+def test_matmul_blocks_grouped_large(bk):
+    lens, n, k = [700, 0, 1900, 33], 3000, 400
+    o = offsets_of(lens, 5)
+    rows = o[-1] + 6
+    x, xs = eight(rows, k, 1)
+    w, ws = zip(*[weights(n, k, False, e) for e in range(len(lens))])
+    y = torch.full((rows, n), 3.25, dtype=F32, device="cuda")
+    bk.matmul_blocks(rows8(x), poison(xs, o).cuda(), rows8(torch.stack(w)), torch.stack(ws).cuda(), bounds(o), out=y)
+    assert (y[: o[0]] == 3.25).all() and (y[o[-1]:] == 3.25).all()
+    for e, n_e in enumerate(lens):
+        if n_e:
+            a, b = o[e], o[e + 1]
+            want, size = blocks_reference(x[a:b], xs[a:b], w[e], ws[e])
+            check_close(y[a:b].cpu(), want, size, k, 4, 128, f"expert {e}")
+
+
 def test_matmul_blocks_of_solver_codes(bk):
     """The solver's codes and steps as an 8-bit operand: the product with V."""
     import oracle
@@ -297,6 +328,76 @@ def test_gradients_are_those_of_the_product(bk):
     tol = 30 * 2.0 ** -23 * size
     assert abs((loss(x2, w) - base - (dx * hx).sum()).item()) <= tol
     assert abs((loss(x, w2) - base - (dw * hw).sum()).item()) <= tol
+
+
+@pytest.mark.parametrize("experts", [129, 1024])
+def test_many_experts(bk, experts):
+    """More experts than tiles are fitted to, most of them short or empty."""
+    g = torch.Generator().manual_seed(experts)
+    lens = torch.randint(0, 4, (experts,), generator=g).tolist()
+    lens[experts // 2] = 150
+    o = offsets_of(lens, 1)
+    rows, n, k = o[-1] + 2, 40, 72
+    x, dy = poison(rand((rows, k), 1, BF16), o).cuda(), poison(rand((rows, n), 2, BF16), o).cuda()
+    w, O = rand((experts, n, k), 3, BF16).cuda(), bounds(o)
+    e = torch.repeat_interleave(torch.arange(experts), torch.tensor(lens)).cuda()
+    a, b = o[0], o[-1]
+    xd, dd, wd = x[a:b].double(), dy[a:b].double(), w.double()[e]
+    y, dx = bk.matmul_grouped(x, w, O), bk.matmul_grouped_dx(dy, w, O)
+    check_close(y[a:b], torch.einsum("tk,tnk->tn", xd, wd), torch.einsum("tk,tnk->tn", xd.abs(), wd.abs()), k, 16, 256, "y")
+    check_close(dx[a:b], torch.einsum("tn,tnk->tk", dd, wd), torch.einsum("tn,tnk->tk", dd.abs(), wd.abs()), n, 16, 256,
+                "dx")
+    outer = lambda p, q: torch.zeros((experts, p.shape[1], q.shape[1]), dtype=torch.float64, device="cuda").index_add_(  # noqa: E731
+        0, e, p[:, :, None] * q[:, None])
+    dw = bk.matmul_grouped_dw(dy, x, O, out_dtype=F32)
+    check_close(dw, outer(dd, xd), outer(dd.abs(), xd.abs()), 150, 16, 256, "dw")
+    count = torch.tensor(lens, dtype=torch.float64, device="cuda").clamp(min=1)[:, None, None]
+    A = bk.gram_grouped(x, O)
+    check_close(A, outer(xd, xd) / count, outer(xd.abs(), xd.abs()) / count, 150, 18, 128, "gram")
+
+
+def test_results_beyond_32_bit_offsets(bk):
+    """Operands and results of more than 2^31 elements, looked at behind there."""
+    rows, n, k = 70001, 32768, 24
+    x, w = rand((rows, k), 1, BF16).cuda(), rand((2, n, k), 2, BF16).cuda()
+    y = bk.matmul_grouped(x, w, bounds([0, 69000, rows]))
+    assert y.numel() > 2 ** 31
+    for a, b, e in ((0, 70, 0), (68950, 69000, 0), (69000, 69050, 1), (rows - 60, rows, 1)):
+        xe, we = x[a:b].double(), w[e].double()
+        check_close(y[a:b], xe @ we.T, xe.abs() @ we.abs().T, k, 16, 256, f"y {a}")
+    # y is now the operand: its last rows lie beyond 2^31 elements
+    dx = bk.matmul_grouped_dx(y, w, bounds([0, 69000, rows]), out_dtype=F32)
+    for a, b, e in ((0, 40, 0), (rows - 40, rows, 1)):
+        de, we = y[a:b].double(), w[e].double()
+        check_close(dx[a:b], de @ we, de.abs() @ we.abs(), n, 16, 512, f"dx {a}")
+    q, s = bk.quantize_blocks(y)
+    for a in (0, rows - 3):
+        want_q, want_s = packed.quantize(y[a:a + 3].cpu(), 1)
+        assert torch.equal(s[a:a + 3].double().cpu(), want_s)
+        assert torch.equal(q[a:a + 3].float().double().cpu(), want_q)
+    q128, s128 = bk.quantize_blocks(y, 128)
+    last = rows // 128 * 128
+    want_q, want_s = packed.quantize(y[last:, :256].cpu(), 128)
+    assert torch.equal(s128[-1:, :2].double().cpu(), want_s)
+    assert torch.equal(q128[last:, :256].float().double().cpu(), want_q)
+    del q128, dx
+    wq, ws = bk.quantize_blocks(rand((96, n), 5, F32).cuda(), 128)
+    z = bk.matmul_blocks(q, s, wq, ws, out_dtype=F32)
+    a = rows - 30
+    xe = q[a:].float().double() * packed.spread(s[a:], n)
+    we = wq.float().double() * packed.spread(ws, n)[:1]
+    check_close(z[a:], xe @ we.T, xe.abs() @ we.abs().T, n, 4, 128, "blocks")
+    del y, q, z
+    experts, d = 33, 8192
+    v = rand((2 * experts, d), 7, BF16).cuda()
+    O = bounds(list(range(0, 2 * experts + 1, 2)))
+    dw = bk.matmul_grouped_dw(v, v, O)
+    assert dw.numel() > 2 ** 31
+    last = v[-2:].double()
+    check_close(dw[-1], last.T @ last, last.abs().T @ last.abs(), 2, 16, 256, "dw")
+    del dw
+    A = bk.gram_grouped(v, O, check_status=False)
+    check_close(A[-1], last.T @ last / 2, last.abs().T @ last.abs() / 2, 2, 18, 128, "gram")
 
 
 # --------------------------------------------------------------- Gram factors
