@@ -7,6 +7,16 @@
 // FP32 samples are split once into three bf16 parts, x = h + m + l to 2^-27 of
 // x; the products hh + (hm + mh) + mm + (hl + lh) on the bf16 tensor cores cost
 // what three TF32 products would and keep 24 bits instead of 21.
+//
+// Tiles are 256 x 256 (256 x 128 from three parts, whose two accumulators fill
+// tensor memory) by CTA pairs; only those that reach the lower triangle are
+// formed, the rest is their mirror image.  A tile costs its group's length, so
+// groups are taken longest first in rounds that run forth and back.
+// Measured: dw of 16384 rows, 8 experts, 4096 x 1024 into fp32 121 us (1.14
+// PFLOP/s; 104 us without its stores); Gram factors of 4 experts at d = 4096
+// from 16384 bf16 rows 266 us (220 without the stores: 268 MB, both halves of
+// every matrix); 8 experts at d = 1024 from 8192 fp32 rows 73 us: 12 to split
+// the samples, 51 for the products, 5 for the damping.
 #include "mm_kernel.cuh"
 
 namespace bakron {

@@ -16,55 +16,59 @@ namespace mm {
 
 namespace {
 
-// Eight consecutive values of a row, as loaded.
+// Sixteen consecutive values of a row, as loaded.
 template <typename T>
-struct alignas(16) Eight {
-    uint32_t w[8 * sizeof(T) / 4];
+struct alignas(32) Run {
+    uint32_t w[16 * sizeof(T) / 4];
 };
 
-// From column c on, zeros from column `cols` on.
-template <typename T>
-__device__ __forceinline__ Eight<T> load8(const T *row, int c, int cols, bool vec)
+__device__ __forceinline__ void load32(const void *p, uint32_t *v)
 {
-    Eight<T> v;
-    if (vec && c + 8 <= cols) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p));
+}
+
+// From column c on, zeros from column `cols` on; `align`: bytes that the row's
+// start is aligned to (32, 16 or less).
+template <typename T>
+__device__ __forceinline__ Run<T> load_run(const T *row, int c, int cols, int align)
+{
+    constexpr int kWords = sizeof(Run<T>::w) / 4;
+    Run<T> v;
+    if (align >= 32 && c + 16 <= cols) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(v.w) / 16; ++i) ((uint4 *)v.w)[i] = __ldg((const uint4 *)(row + c) + i);
+        for (int i = 0; i < kWords; i += 8) load32((const uint32_t *)(row + c) + i, v.w + i);
+    } else if (align >= 16 && c + 16 <= cols) {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 4) *(uint4 *)(v.w + i) = __ldg((const uint4 *)((const uint32_t *)(row + c) + i));
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v.w[i] = c + i < cols ? __float_as_uint(row[c + i]) : 0u;
+        for (int i = 0; i < 16; ++i) v.w[i] = c + i < cols ? __float_as_uint(row[c + i]) : 0u;
     } else {
         const uint16_t *h = (const uint16_t *)row;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
             const uint32_t lo = c + 2 * i < cols ? h[c + 2 * i] : 0u, hi = c + 2 * i + 1 < cols ? h[c + 2 * i + 1] : 0u;
             v.w[i] = lo | (hi << 16);
         }
     }
     return v;
 }
+__device__ __forceinline__ int row_align(const void *row)
+{
+    return ((uintptr_t)row & 31) == 0 ? 32 : ((uintptr_t)row & 15) == 0 ? 16 : 1;
+}
 
-__device__ __forceinline__ void to_floats(const Eight<float> &e, float (&v)[8])
+// The two numbers of word i of a 16-bit run.
+__device__ __forceinline__ float2 pair_of(const Run<__nv_bfloat16> &e, int i)
 {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(e.w[i]);
+    return make_float2(__uint_as_float(e.w[i] << 16), __uint_as_float(e.w[i] & 0xffff0000u));
 }
-__device__ __forceinline__ void to_floats(const Eight<__nv_bfloat16> &e, float (&v)[8])
+__device__ __forceinline__ float2 pair_of(const Run<__half> &e, int i) { return __half22float2(*(const __half2 *)&e.w[i]); }
+__device__ __forceinline__ float2 pair_of(const Run<float> &e, int i)
 {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(e.w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(e.w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void to_floats(const Eight<__half> &e, float (&v)[8])
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*(const __half2 *)&e.w[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
+    return make_float2(__uint_as_float(e.w[2 * i]), __uint_as_float(e.w[2 * i + 1]));
 }
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
@@ -74,11 +78,11 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
     return m;
 }
 
-// The largest magnitude of the eight values and `most`, as the bits of the type
+// The largest magnitude of the values and `most`, as the bits of the type
 // with the sign cleared: ordered like the magnitudes, infinities and NaN above
 // every finite value.  16-bit types keep two maxima in one word.
 template <typename T>
-__device__ __forceinline__ uint32_t most_of(const Eight<T> &e, uint32_t most)
+__device__ __forceinline__ uint32_t most_of(const Run<T> &e, uint32_t most)
 {
 #pragma unroll
     for (int i = 0; i < (int)sizeof(e.w) / 4; ++i)
@@ -97,11 +101,9 @@ __device__ __forceinline__ float most_value(uint32_t most)
     if constexpr (sizeof(T) == 4) {
         return __uint_as_float(most);
     } else {
-        Eight<T> e{};
+        Run<T> e{};
         e.w[0] = max(most & 0xffffu, most >> 16);
-        float v[8];
-        to_floats(e, v);
-        return v[0];
+        return pair_of(e, 0).x;
     }
 }
 
@@ -111,78 +113,78 @@ __device__ __forceinline__ float step_of(float most)
     return s == 0.f ? 1.f : s;
 }
 
-// rs: 1 / s correctly rounded.
+// The codes of a run; rs: 1 / s correctly rounded.
 template <typename T>
-__device__ __forceinline__ void store8(uint8_t *row, int c, int cols, const Eight<T> &e, float s, float rs)
+__device__ __forceinline__ void store_codes(uint8_t *row, int c, int cols, const Run<T> &e, float s, float rs)
 {
-    float v[8];
-    to_floats(e, v);
     // div_rn_recip is exact for steps in [2^-60, 2^60] wherever the code is not zero
-    if (s >= 0x1p-60f && s <= 0x1p60f) {
+    const bool fast = s >= 0x1p-60f && s <= 0x1p60f;
+    uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = div_rn_recip(v[i], s, rs);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(v[i], s);
-    }
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i], v[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi =
-            __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2], v[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
+    for (int i = 0; i < 4; ++i) {
+        float2 a = pair_of(e, 2 * i), b = pair_of(e, 2 * i + 1);
+        if (fast) {
+            a = make_float2(div_rn_recip(a.x, s, rs), div_rn_recip(a.y, s, rs));
+            b = make_float2(div_rn_recip(b.x, s, rs), div_rn_recip(b.y, s, rs));
+        } else {
+            a = make_float2(__fdiv_rn(a.x, s), __fdiv_rn(a.y, s));
+            b = make_float2(__fdiv_rn(b.x, s), __fdiv_rn(b.y, s));
+        }
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
         w[i] = lo | (hi << 16);
     }
-    if (c + 8 <= cols) {
-        *(uint2 *)(row + c) = make_uint2(w[0], w[1]);
+    if (c + 16 <= cols) {
+        *(uint4 *)(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 16; ++i)
             if (c + i < cols) row[c + i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
     }
 }
 
 // One step per row and 128 columns.  A warp takes 1024 columns of one row (the
-// grid's x: eight rows a CTA, y: strips of columns): 16 threads per block of 8
-// values each, four blocks in flight per thread.
+// grid's x: eight rows a CTA, y: strips of columns): 8 threads per block of 16
+// values each, two blocks per thread in flight.  Bound by its bytes (4 + 1 or
+// 2 + 1 per value) once each value takes few enough instructions: with eight
+// values a thread and the steps computed by every lane it issued 19 per value
+// and took 95 us for 16384 x 4096 in bf16.
 constexpr int kStrip = 1024;
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a)
 {
     // (columns fit 32 bits: at most 2^30)
     const int cols = (int)a.cols, kblocks = (cols + 127) / 128, strips = (cols + kStrip - 1) / kStrip;
-    const int lane = threadIdx.x & 31, sub = lane & 15;
+    const int lane = threadIdx.x & 31, sub = lane & 7;
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (row >= a.batch * a.rows) return;
     const int64_t e = a.batch > 1 ? row / a.rows : 0, r = row - e * a.rows;
     const T *src = (const T *)a.x + e * a.x_batch_stride + r * a.x_row_stride;
     uint8_t *dst = a.q + row * a.q_row_stride;
     float *steps = a.steps + row * kblocks;
-    const bool vec = ((uintptr_t)src & 15) == 0;
+    const int align = row_align(src);
     bool finite = true;
     for (int strip = blockIdx.y; strip < strips; strip += gridDim.y) {
-        Eight<T> v[4];
-        uint32_t most[4];
+        Run<T> v[2];
+        uint32_t most[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = load8(src, strip * kStrip + i * 256 + lane * 8, cols, vec);
+        for (int i = 0; i < 2; ++i) v[i] = load_run(src, strip * kStrip + i * 512 + lane * 16, cols, align);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) most[i] = most_of(v[i], 0u);
+        for (int i = 0; i < 2; ++i) most[i] = most_of(v[i], 0u);
 #pragma unroll
-        for (int o = 8; o; o >>= 1)
+        for (int o = 4; o; o >>= 1)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) most[i] = most2<T>(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
-        // the warp's eight steps: one per lane, then handed round (computed by
-        // every lane for itself, the divisions were a third of the instructions)
-        const uint32_t own = sub & 2 ? (sub & 1 ? most[3] : most[2]) : (sub & 1 ? most[1] : most[0]);
-        const float m = most_value<T>(own), s_own = step_of(m), rs_own = __frcp_rn(s_own);
+            for (int i = 0; i < 2; ++i) most[i] = most2<T>(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
+        // the warp's eight steps: one per lane, then handed round
+        const float m = most_value<T>(sub & 1 ? most[1] : most[0]), s_own = step_of(m), rs_own = __frcp_rn(s_own);
         finite &= isfinite(m);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float s = __shfl_sync(0xffffffffu, s_own, (lane & 16) | i);
-            const float rs = __shfl_sync(0xffffffffu, rs_own, (lane & 16) | i);
-            const int kb = strip * (kStrip / 128) + i * 2 + (lane >> 4);
+        for (int i = 0; i < 2; ++i) {
+            const float s = __shfl_sync(0xffffffffu, s_own, (lane & 24) | i);
+            const float rs = __shfl_sync(0xffffffffu, rs_own, (lane & 24) | i);
+            const int kb = strip * (kStrip / 128) + i * 4 + (lane >> 3);
             if (kb < kblocks) {
-                store8(dst, kb * 128 + sub * 8, cols, v[i], s, rs);
+                store_codes(dst, kb * 128 + sub * 16, cols, v[i], s, rs);
                 if (sub == 0) steps[kb] = s;
             }
         }
@@ -192,23 +194,23 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a)
 
 // One step per 128 x 128 tile: one CTA per tile, its values in registers
 // between the two passes.
-constexpr int kTileThreads = 512, kTileRows = kTileThreads / 16, kTileLoads = 128 / kTileRows;
+constexpr int kTileThreads = 512, kTileRows = kTileThreads / 8, kTileLoads = 128 / kTileRows;
 template <typename T>
 __global__ void __launch_bounds__(kTileThreads, 2) quantize_tiles_kernel(const QuantArgs a)
 {
     __shared__ uint32_t part[kTileThreads / 32];
     const unsigned kblocks = (unsigned)((a.cols + 127) / 128), rblocks = (unsigned)((a.rows + 127) / 128);
     const unsigned kb = blockIdx.x % kblocks, eb = blockIdx.x / kblocks, e = eb / rblocks, rb = eb - e * rblocks;
-    const int sub = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+    const int sub = threadIdx.x & 7, r0 = threadIdx.x >> 3;
     const T *src = (const T *)a.x + e * a.x_batch_stride;
-    const bool vec = (((uintptr_t)src | (uintptr_t)(a.x_row_stride * (int64_t)sizeof(T))) & 15) == 0;
-    const int c = (int)(kb * 128 + sub * 8);
-    Eight<T> v[kTileLoads];
+    const int align = min(row_align(src), row_align((const void *)(uintptr_t)(a.x_row_stride * (int64_t)sizeof(T))));
+    const int c = (int)(kb * 128 + sub * 16);
+    Run<T> v[kTileLoads];
     uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < kTileLoads; ++i) {
         const int64_t r = (int64_t)rb * 128 + r0 + kTileRows * i;
-        v[i] = load8(src + r * a.x_row_stride, c, r < a.rows ? (int)a.cols : 0, vec);
+        v[i] = load_run(src + r * a.x_row_stride, c, r < a.rows ? (int)a.cols : 0, align);
     }
 #pragma unroll
     for (int i = 0; i < kTileLoads; ++i) most = most_of(v[i], most);
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) quantize_tiles_kernel(const Q
 #pragma unroll
     for (int i = 0; i < kTileLoads; ++i) {
         const int64_t r = (int64_t)rb * 128 + r0 + kTileRows * i;
-        if (r < a.rows) store8(a.q + ((int64_t)e * a.rows + r) * a.q_row_stride, c, (int)a.cols, v[i], s, rs);
+        if (r < a.rows) store_codes(a.q + ((int64_t)e * a.rows + r) * a.q_row_stride, c, (int)a.cols, v[i], s, rs);
     }
     if (threadIdx.x == 0) a.steps[(int64_t)eb * kblocks + kb] = s;
 }
