@@ -309,7 +309,7 @@ bakron_status_t bakron_matmul_blocks(const uint8_t *x_dev, int64_t x_row_stride,
     if (!map2(xm, t, 1, x_dev, k, rows, x_row_stride, 128, small ? 32 : 128) ||
         (small && !map2(&maps.b2, t, 1, x_dev, k, rows, x_row_stride, 128, 64)) ||
         !map3(wm, t, 1, w_dev, k, n, w_row_stride, experts, w_expert_stride, 128,
-              small ? 128 : v == kEightPair256 ? 64 : (uint32_t)(bn * 128 / m)))
+              small ? 128 : (uint32_t)(bn * 128 / m)))
         return BAKRON_ERR_CUDA;
     if (launch_eight(v, maps, g, tiles, sms, (cudaStream_t)stream) !=
         cudaSuccess)

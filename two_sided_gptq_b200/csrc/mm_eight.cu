@@ -6,7 +6,7 @@
 // (row step x weight step) times the chunk into its FP32 registers.  That chain
 // -- MMA, commit, read, add, hand the buffer back -- takes about 2000 clocks
 // whatever the tile, so its chunks in flight set the rate: two of 256 columns
-// (each in two halves with barriers of their own) or four of 128.  Measured per
+// or four of 128.  Measured per
 // chunk (8192 x 14336 x 4096): 1004 clocks at 256 x 256 (512 at the MMA peak,
 // 770 without the additions, 684 without reading the accumulators at all: the
 // operand loads, 48 bytes per clock and SM), 602 at 256 x 128, 630 at 128 x 128.

@@ -79,10 +79,6 @@ struct Shape {
     // clocks, whatever the tile) is shared by several chunks
     static constexpr int kBufs = P::kEight ? (P::kBN == 256 ? 2 : 4) : 2;
     static constexpr int kTmemCols = kBufs * kAcc * P::kBN;
-    // with only two of them and short chunks the tile's two column halves are
-    // separate MMAs with separate barriers, so that each is read out while the
-    // other is computed
-    static constexpr int kHalves = P::kEight && P::kBN == 256 ? 2 : 1;
     static constexpr int kThreads = 128 + 32 * kEpiWarps;
     // registers: the epilogue's accumulators and two loads in flight need more
     // than a 12-warp CTA's even share (168), the other warps far less
@@ -425,10 +421,10 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     auto empty_bar = [&](int s) { return bar0 + 8u * (S::kStages + s); };
     auto tail_full_bar = [&](int s) { return bar0 + 8u * (2 * S::kStages + s); };  // a tail stage has landed in this CTA
     auto tail_done_bar = [&](int s) { return bar0 + 8u * (3 * S::kStages + s); };  // the CTAs have zeroed their tails
-    auto accf_bar = [&](int b, int h) { return bar0 + 8u * (4 * S::kStages + S::kBufs * h + b); };
-    auto acce_bar = [&](int b, int h) { return bar0 + 8u * (4 * S::kStages + S::kBufs * (S::kHalves + h) + b); };
-    const uint32_t drain_bar = bar0 + 8u * (4 * S::kStages + 2 * S::kBufs * S::kHalves);
-    static_assert(4 * S::kStages + 2 * S::kBufs * S::kHalves + 1 <= 48, "barriers");
+    auto accf_bar = [&](int b) { return bar0 + 8u * (4 * S::kStages + b); };
+    auto acce_bar = [&](int b) { return bar0 + 8u * (4 * S::kStages + S::kBufs + b); };
+    const uint32_t drain_bar = bar0 + 8u * (4 * S::kStages + 2 * S::kBufs);
+    static_assert(4 * S::kStages + 2 * S::kBufs + 1 <= 48, "barriers");
     // accumulator chunk number c: its buffer and the parity of its buffer's use
     auto buf_of = [](int c) { return c % S::kBufs; };
     auto use_of = [](int c) { return c / S::kBufs & 1; };
@@ -442,11 +438,10 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             mbar_init(tail_full_bar(s), 1);
             mbar_init(tail_done_bar(s), S::kCtas);
         }
-        for (int b = 0; b < S::kBufs; ++b)
-            for (int h = 0; h < S::kHalves; ++h) {
-                mbar_init(accf_bar(b, h), 1);
-                mbar_init(acce_bar(b, h), S::kEpiWarps * S::kCtas / S::kHalves);
-            }
+        for (int b = 0; b < S::kBufs; ++b) {
+            mbar_init(accf_bar(b), 1);
+            mbar_init(acce_bar(b), S::kEpiWarps * S::kCtas);
+        }
         mbar_init(drain_bar, 1);
         abort_sh = 0;
         error_sh = 0;
@@ -609,10 +604,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                         }
                     } else if (P::kRagged == kTokensA) {
                         load2(a, &maps.a, k, a0);
-#pragma unroll
-                        for (int h = 0; h < S::kHalves; ++h)
-                            load3(b + h * S::kBBytes / S::kHalves, &maps.b, k,
-                                  x.b0 + (h * S::kCtas + rank) * (S::kBRows / S::kHalves), x.e);
+                        load3(b, &maps.b, k, b0, x.e);
                     } else {
 #pragma unroll
                         for (int p = 0; p < P::kPlanes; ++p) {
@@ -666,14 +658,13 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             for (int t = tile0; t < total && ok; t = next_tile(t)) {
                 const Tile x = find_tile<P>(g, first, order, t);
                 const int nkb = ceil_div(x.k1 - x.k0, S::kKB);
-                const int n_mma = P::kRagged == kTokensB ? (x.nb + 15) & ~15 : BN / S::kHalves;
+                const int n_mma = P::kRagged == kTokensB ? (x.nb + 15) & ~15 : BN;
                 const uint32_t idesc = g.idesc | ((uint32_t)(n_mma >> 3) << 17) | ((uint32_t)(S::kM >> 4) << 24);
                 const int kb0 = stage_begin(nkb), kb1 = stage_end(nkb);
                 for (int kb = kb0, in_chunk = 0; kb < kb1; ++kb, ++it) {
                     const int buf = buf_of(chunk);
                     const int s = it % S::kStages;
-                    if (S::kHalves == 1 && in_chunk == 0 && chunk >= S::kBufs)
-                        ok = wait(acce_bar(buf, 0), use_of(chunk) ^ 1);
+                    if (in_chunk == 0 && chunk >= S::kBufs) ok = wait(acce_bar(buf), use_of(chunk) ^ 1);
                     ok = ok && wait(full_bar(s), (it / S::kStages) & 1);
                     int steps = kSteps;
                     if (P::kRagged == kContract) {
@@ -692,47 +683,30 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                     const uint32_t d = tmem_base + (uint32_t)(buf * S::kAcc * BN);
                     const uint64_t ad = a_desc + (uint32_t)(s * (S::kStageBytes >> 4));
                     const uint64_t bd = b_desc + (uint32_t)(s * (S::kStageBytes >> 4));
-                    if constexpr (S::kHalves > 1) {
 #pragma unroll
-                        for (int h = 0; h < S::kHalves; ++h) {
-                            ok = ok && (chunk < S::kBufs || wait(acce_bar(buf, h), use_of(chunk) ^ 1));
-                            if (!ok) break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int ks = 0; ks < kSteps; ++ks)
-                                mma(d + h * (BN / S::kHalves), ad + ks * kAStep,
-                                    bd + ks * kBStep + h * (S::kBBytes / S::kHalves >> 4), idesc, ks != 0);
-                            commit(accf_bar(buf, h));
+                    for (int ks = 0; ks < kSteps; ++ks) {
+                        if (P::kRagged == kContract && ks >= steps) break;
+                        const uint32_t add = (in_chunk | ks) != 0;
+                        const uint64_t ak = ad + ks * kAStep, bk = bd + ks * kBStep;
+                        if (P::kPlanes > 1) {
+                            // x = h + m + l in three bf16 parts: hh into one
+                            // accumulator, the five smaller products into another
+                            constexpr uint32_t kAm = S::kABytes >> 4, kBm = S::kBBytes >> 4;
+                            mma(d, ak, bk, idesc, add);
+                            mma(d + BN, ak, bk + 2 * kBm, idesc, add);
+                            mma(d + BN, ak + 2 * kAm, bk, idesc, 1);
+                            mma(d + BN, ak + kAm, bk + kBm, idesc, 1);
+                            mma(d + BN, ak, bk + kBm, idesc, 1);
+                            mma(d + BN, ak + kAm, bk, idesc, 1);
+                        } else {
+                            mma(d, ak, bk, idesc, add);
                         }
-                        if (!ok) break;
-                        commit(empty_bar(s));
+                    }
+                    commit(empty_bar(s));
+                    if (++in_chunk == chunk_stages || kb == kb1 - 1) {
+                        commit(accf_bar(buf));
+                        in_chunk = 0;
                         ++chunk;
-                    } else {
-#pragma unroll
-                        for (int ks = 0; ks < kSteps; ++ks) {
-                            if (P::kRagged == kContract && ks >= steps) break;
-                            const uint32_t add = (in_chunk | ks) != 0;
-                            const uint64_t ak = ad + ks * kAStep, bk = bd + ks * kBStep;
-                            if (P::kPlanes > 1) {
-                                // x = h + m + l in three bf16 parts: hh into one
-                                // accumulator, the five smaller products into another
-                                constexpr uint32_t kAm = S::kABytes >> 4, kBm = S::kBBytes >> 4;
-                                mma(d, ak, bk, idesc, add);
-                                mma(d + BN, ak, bk + 2 * kBm, idesc, add);
-                                mma(d + BN, ak + 2 * kAm, bk, idesc, 1);
-                                mma(d + BN, ak + kAm, bk + kBm, idesc, 1);
-                                mma(d + BN, ak, bk + kBm, idesc, 1);
-                                mma(d + BN, ak + kAm, bk, idesc, 1);
-                            } else {
-                                mma(d, ak, bk, idesc, add);
-                            }
-                        }
-                        commit(empty_bar(s));
-                        if (++in_chunk == chunk_stages || kb == kb1 - 1) {
-                            commit(accf_bar(buf, 0));
-                            in_chunk = 0;
-                            ++chunk;
-                        }
                     }
                 }
             }
@@ -772,7 +746,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
         const int lane_row = rank * kBM + quad * 32 + lane, col0 = half * S::kCols;
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
         float *steps_w = steps_sh + (warp - 4) * S::kStepFloats;
-        const uint32_t first_cta_acce = kPair ? map_rank(acce_bar(0, 0), 0) : acce_bar(0, 0);
+        const uint32_t first_cta_acce = kPair ? map_rank(acce_bar(0), 0) : acce_bar(0);
         int chunk = 0;
         bool ok = true;
         for (int t = tile0; t < total && ok; t = next_tile(t)) {
@@ -800,11 +774,10 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                                       min((x.a0 + rank * kBM) / 128, ceil_div(g.a_total, 128) - 1)) * nkb;
                 }
             }
-            const int bar_half = S::kHalves > 1 ? half : 0;
             // One chunk: wait for it, add it, give its buffer back.
             auto take = [&](float row_step, const float *steps) {
                 const int buf = buf_of(chunk);
-                ok = wait(accf_bar(buf, bar_half), use_of(chunk)) && ok;
+                ok = wait(accf_bar(buf), use_of(chunk)) && ok;
                 __syncwarp();
                 tc_fence_after();
                 const uint32_t src = tmem_base + lane_off + (uint32_t)(buf * S::kAcc * BN + col0);
@@ -825,7 +798,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        const uint32_t bar = first_cta_acce + 8u * (S::kBufs * bar_half + buf);
+                        const uint32_t bar = first_cta_acce + 8u * buf;
                         if (kPair) mbar_arrive_remote(bar);
                         else mbar_arrive(bar);
                     }
