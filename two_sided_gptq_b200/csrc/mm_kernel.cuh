@@ -62,9 +62,9 @@ struct Shape {
     static constexpr int kABytes = P::kRagged == kContract ? kBM / 64 * kKB * 128 : kBM * 128;
     static constexpr int kBBytes = P::kRagged == kContract ? kBRows / 64 * kKB * 128 : kBRows * 128;
     static constexpr int kStageBytes = P::kPlanes * (kABytes + kBBytes);
-    // shared memory in which results are turned (store_turned)
+    // shared memory in which results are turned (store_turned, store_staged)
     static constexpr bool kTurn = P::kRagged == kTokensB && P::kBN == 256;
-    static constexpr int kTurnSpace = kTurn ? 2 * 32 * kBM * 2 : 0;
+    static constexpr int kTurnSpace = kTurn ? 2 * 32 * kBM * 2 : P::kRagged == kTokensB ? 0 : 8 * 32 * 17 * 4;
     static constexpr int kEpiWarps = 8;
     static constexpr int kCols = P::kBN / (kEpiWarps / 4);          // columns per epilogue thread
     // a warp's staged steps: two chunks of its columns' (kTokensB), or one of them
@@ -228,49 +228,83 @@ __device__ __forceinline__ uint32_t word_of<__half>(float lo, float hi)
     return *(const uint32_t *)&v;
 }
 
+// Columns [0, cols) of a warp's 32 rows (the lanes'; `rows` of them valid, the
+// first at `first`), N columns of each in its lane's registers, through the
+// warp's own shared memory, so that stores run along the rows: for results whose
+// rows are not 32-byte aligned.  (Written from the lanes' own rows, every store
+// touches 32 sectors: it took ten times as long.)
+constexpr int kStageWords = 32 * 17;
+template <typename T, int N, class Value, class Keep>
+__device__ __forceinline__ void store_staged(T *first, int64_t ld, int rows, int cols, int lane, uint32_t *buf,
+                                             Value value, Keep keep)
+{
+    constexpr int kWide = 64 / sizeof(T);  // columns a round: 16 words per row
+#pragma unroll
+    for (int c0 = 0; c0 < N; c0 += kWide) {
+        if (c0 >= cols) break;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+            if constexpr (sizeof(T) == 4) buf[lane * 17 + w] = __float_as_uint(value(c0 + w));
+            else buf[lane * 17 + w] = word_of<T>(value(c0 + 2 * w), value(c0 + 2 * w + 1));
+        }
+        __syncwarp();
+        constexpr int kRows = 32 / kWide;  // rows a store covers
+        const int c = lane % kWide;
+        if (c0 + c < cols) {
+#pragma unroll 4
+            for (int r = lane / kWide; r < rows; r += kRows)
+                if (keep(r, c0 + c)) first[r * ld + c0 + c] = ((const T *)(buf + r * 17))[c];
+        }
+        __syncwarp();
+    }
+}
+
 // Store this thread's accumulators: D row `lane_row` of the tile, columns
-// [col0, col0 + N).
+// [col0, col0 + N).  All lanes of the warp take part.
 template <class P, typename T, int N>
 __device__ __forceinline__ void store_tile(const Args &g, const Tile &x, int lane_row, int col0,
-                                           const float (&acc)[N])
+                                           const float (&acc)[N], uint32_t *buf)
 {
-    constexpr int C = N;
     T *out = (T *)g.out;
-    if (lane_row >= x.na) return;
+    const int cols = min(N, x.nb - col0);
     if (P::kRagged == kTokensB) {
         // D row = output column: the 32 lanes of a warp write consecutive
         // elements of one packed row
+        if (lane_row >= x.na) return;
         T *p = out + (int64_t)(x.b0 + col0) * g.ldo + x.a0 + lane_row;
         float s = 1.f;
         if (P::kEight && g.w_step_rows == 1) s = __ldg(g.w_steps + (int64_t)x.e * g.a_total + x.a0 + lane_row);
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-            if (col0 + c < x.nb) {
-                const float v = acc[c];
-                p[(int64_t)c * g.ldo] = round_to<T>(P::kEight ? v * s : v);
-            }
+        for (int c = 0; c < N; ++c)
+            if (c < cols) p[(int64_t)c * g.ldo] = round_to<T>(P::kEight ? acc[c] * s : acc[c]);
     } else {
-        T *p = out + (P::kRagged == kContract ? (int64_t)x.e * g.out_expert_stride : 0) +
-               (int64_t)(x.a0 + lane_row) * g.ldo + x.b0 + col0;
-        const int n = min(C, x.nb - col0);
-        auto value = [&](int c) { return acc[c]; };
-        if (n == C && ((uintptr_t)p & 31) == 0) {
-            // one whole 32-byte sector per store
-            constexpr int kVec = 32 / sizeof(T);
+        T *tile = out + (P::kRagged == kContract ? (int64_t)x.e * g.out_expert_stride : 0) + (int64_t)x.a0 * g.ldo +
+                  x.b0 + col0;
+        const uintptr_t align = (uintptr_t)tile | (uintptr_t)(g.ldo * (int64_t)sizeof(T));  // of every row
+        if (align & 31) {
+            const int lane = threadIdx.x & 31;
+            store_staged<T, N>(tile + (int64_t)(lane_row - lane) * g.ldo, g.ldo, min(32, x.na - (lane_row - lane)), cols,
+                               lane, buf, [&](int c) { return acc[c]; }, [](int, int) { return true; });
+            return;
+        }
+        if (lane_row >= x.na) return;
+        T *p = tile + (int64_t)lane_row * g.ldo;
+        constexpr int kVec = 32 / sizeof(T);
 #pragma unroll
-            for (int c = 0; c < C; c += kVec) {
+        for (int c = 0; c < N; c += kVec) {
+            if (c + kVec <= cols) {
                 uint32_t v[8];
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    if constexpr (sizeof(T) == 4) v[u] = __float_as_uint(value(c + u));
-                    else v[u] = word_of<T>(value(c + 2 * u), value(c + 2 * u + 1));
+                    if constexpr (sizeof(T) == 4) v[u] = __float_as_uint(acc[c + u]);
+                    else v[u] = word_of<T>(acc[c + 2 * u], acc[c + 2 * u + 1]);
                 }
-                store32(p + c, v);
-            }
-        } else {
+                store32(p + c, v);  // one whole 32-byte sector
+            } else {
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (c < n) p[c] = round_to<T>(value(c));
+                for (int u = 0; u < kVec; ++u)
+                    if (c + u < cols) p[c + u] = round_to<T>(acc[c + u]);
+            }
         }
     }
 }
@@ -323,37 +357,47 @@ __device__ __forceinline__ void store_turned(const Args &g, const Tile &x, int r
 }
 
 // Gram tile: entries on and below the diagonal, divided by the group's count,
-// and their mirror images.
+// and their mirror images.  All lanes of the warp take part.
 template <int N>
 __device__ __forceinline__ void store_gram(const Args &g, const Tile &x, int lane_row, int col0,
-                                           const float (&acc)[N])
+                                           const float (&acc)[N], uint32_t *buf)
 {
-    if (lane_row >= x.na) return;
     const int64_t d = g.ldo;
     float *out = (float *)g.out + (int64_t)x.e * g.out_expert_stride;
-    const int i = x.a0 + lane_row, j0 = x.b0 + col0;
+    const int lane = threadIdx.x & 31, i = x.a0 + lane_row, j0 = x.b0 + col0;
     const float count = (float)max(x.count, 1), rcount = __frcp_rn(count);
     auto value = [&](int c) { return div_rn_recip(acc[c], count, rcount); };
-    float *row = out + i * d + j0, *col = out + j0 * d + i;
-    const bool vec = ((uintptr_t)row & 31) == 0;
-    // Eight columns at a time: whole 32-byte sectors along the row where all
-    // eight are below the diagonal, and a warp's 32 rows next to each other in
-    // the mirror image.
+    // columns of this row up to the diagonal
+    const int cols = lane_row < x.na ? min(x.nb - col0, i + 1 - j0) : 0;
+    float *col = out + j0 * d + i;
+    const uintptr_t align = (uintptr_t)(out + j0) | (uintptr_t)(d * 4);
+    if (align & 31) {
+        // the mirror image runs along the lanes as it is
+#pragma unroll
+        for (int c = 0; c < N; ++c)
+            if (c < cols) col[(int64_t)c * d] = value(c);
+        const int row0 = lane_row - lane;  // the warp's first row
+        store_staged<float, N>(out + (int64_t)(x.a0 + row0) * d + j0, d, min(32, x.na - row0), min(N, x.nb - col0), lane,
+                               buf, value, [&](int r, int c) { return j0 + c <= x.a0 + row0 + r; });
+        return;
+    }
+    float *row = out + i * d + j0;
+    // Eight columns at a time: along the row where all eight are below the
+    // diagonal, and a warp's 32 rows next to each other in the mirror image.
 #pragma unroll
     for (int c = 0; c < N; c += 8) {
-        const int n = min(x.nb - col0, i + 1 - j0) - c;  // columns of these that are written
-        if (n >= 8 && vec) {
+        if (c + 8 <= cols) {
             uint32_t v[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 v[u] = __float_as_uint(value(c + u));
                 col[(int64_t)(c + u) * d] = __uint_as_float(v[u]);
             }
-            store32(row + c, v);
-        } else if (n > 0) {
+            store32(row + c, v);  // one whole 32-byte sector
+        } else {
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                if (u < n) {
+                if (c + u < cols) {
                     const float v = value(c + u);
                     row[c + u] = v;
                     col[(int64_t)(c + u) * d] = v;
@@ -746,6 +790,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
         const int lane_row = rank * kBM + quad * 32 + lane, col0 = half * S::kCols;
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
         float *steps_w = steps_sh + (warp - 4) * S::kStepFloats;
+        uint32_t *stage_buf = (uint32_t *)turn_sh + (warp - 4) * kStageWords;  // (not with kTokensB)
         const uint32_t first_cta_acce = kPair ? map_rank(acce_bar(0), 0) : acce_bar(0);
         int chunk = 0;
         bool ok = true;
@@ -908,7 +953,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                 for (int c = 0; c < S::kCols; ++c) acc[c] *= steps_w[c];
             }
             if constexpr (P::kLower) {
-                store_gram(g, x, lane_row, col0, acc);
+                store_gram(g, x, lane_row, col0, acc, stage_buf);
                 continue;
             }
             if constexpr (S::kTurn) {
@@ -921,9 +966,9 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                     continue;
                 }
             }
-            if (g.out_type == BAKRON_BF16) store_tile<P, __nv_bfloat16>(g, x, lane_row, col0, acc);
-            else if (g.out_type == BAKRON_F16) store_tile<P, __half>(g, x, lane_row, col0, acc);
-            else store_tile<P, float>(g, x, lane_row, col0, acc);
+            if (g.out_type == BAKRON_BF16) store_tile<P, __nv_bfloat16>(g, x, lane_row, col0, acc, stage_buf);
+            else if (g.out_type == BAKRON_F16) store_tile<P, __half>(g, x, lane_row, col0, acc, stage_buf);
+            else store_tile<P, float>(g, x, lane_row, col0, acc, stage_buf);
         }
     }
     if constexpr (S::kSplit) {
