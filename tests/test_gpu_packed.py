@@ -425,6 +425,39 @@ def test_gram_grouped(bk, lens, lead, tail, d, dtype):
                     f"gram {e}")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("lens,lead,tail,n,k", [
+    ([4099], 0, 0, 130, 72),             # one or a few tiles: eight CTAs share each
+    ([1, 3001, 0, 79], 3, 5, 200, 131),  # ... with groups shorter than the parts
+    ([5, 517, 1030], 0, 9, 1300, 257),   # fewer CTAs per tile
+    ([700, 3, 1411, 260, 0, 517, 90, 333, 1601], 1, 7, 1003, 1130),  # tiles of CTA pairs
+])
+def test_contractions_over_rows(bk, lens, lead, tail, n, k, dtype):
+    """dw and Gram factors by every tile shape and split, results with odd rows."""
+    o = offsets_of(lens, lead)
+    rows = o[-1] + tail
+    x = poison((rand((rows, k), k) * torch.exp(rand((1, k), 8))).to(dtype), o)
+    X, O = rows_of(x, 8), bounds(o)
+    A = bk.gram_grouped(X, O)
+    assert torch.equal(A, A.transpose(1, 2)) and torch.equal(A, bk.gram_grouped(X, O))
+    if dtype != F32:
+        dy = poison(rand((rows, n), n, dtype), o)
+        D = rows_of(dy, 8)
+        dw = {t: bk.matmul_grouped_dw(D, X, O, out_dtype=t) for t in (dtype, F32)}
+        assert torch.equal(dw[F32], bk.matmul_grouped_dw(D, X, O, out_dtype=F32))
+    for e, n_e in enumerate(lens):
+        if not n_e:
+            assert (A[e] == 0).all()
+            continue
+        xe = x[o[e]:o[e + 1]].cuda().double()
+        check_close(A[e], xe.T @ xe / n_e, xe.abs().T @ xe.abs() / n_e, n_e, 18, 128, f"gram {e}")
+        if dtype == F32:
+            continue
+        de = dy[o[e]:o[e + 1]].cuda().double()
+        for t in dw:
+            check_close(dw[t][e], de.T @ xe, de.abs().T @ xe.abs(), n_e, 16, 256, f"dw {e} {t}")
+
+
 def test_gram_grouped_is_gram_for_one_group(bk):
     x = rand((1000, 300), 2).cuda()
     A, one = bk.gram_grouped(x, bounds([0, 1000]), 0.01)[0], bk.gram(x, 0.01)

@@ -40,8 +40,9 @@ struct Args {
 enum Variant {
     kRows256, kRows64,          // y = x w^T: packed rows on D's columns, tiles of 256 / 64
     kRowsDx256, kRowsDx64,      // dx = dy w
-    kOuter,                     // dw = dy^T x
-    kGramOne, kGramThree,       // X^T X from 16-bit samples / from three bf16 parts of fp32
+    kOuterPair, kOuterOne,      // dw = dy^T x, by tiles of a CTA pair / of one CTA
+    kGramPair, kGramOne,        // X^T X from 16-bit samples
+    kGramThreePair, kGramThreeOne,  // X^T X from three bf16 parts of fp32 samples
     kEightPair256, kEightPair128, kEightOne128,  // 8-bit operands, packed rows on D's rows: 256 of them
                                                  // (a CTA pair) or 128, by 256 or 128 columns
     kEightB64                                    // packed rows on D's columns

@@ -161,6 +161,32 @@ Variant eight_variant(int64_t rows, int64_t n, int64_t k, int64_t experts, int s
     return best;
 }
 
+// Products over the packed rows of a group: CTA pairs' tiles (256 x `width`), or
+// one CTA's (128 x 128), of which up to eight CTAs may share one; whichever needs
+// the least time, as above, at the clocks per `step` rows of the contraction.
+// `tiles` is replaced by the number of the tiles taken.
+bool outer_pair(int64_t rows, int64_t experts, int64_t pair_tiles, int64_t one_tiles, int64_t step, double pair_clocks,
+                double one_clocks, int sms, int64_t &tiles, int &split)
+{
+    const double store = 2500, join = 1800;
+    const int64_t steps = ceil64(ceil64(rows, experts), step);
+    double least = ceil64(2 * pair_tiles, sms) * (steps * pair_clocks + 2 * store);
+    bool pair = true;
+    tiles = pair_tiles;
+    split = 1;
+    for (int p = 1; p <= 8; p *= 2) {
+        if (p > 1 && (one_tiles * p > sms || steps < 2 * p)) break;
+        const double cost = ceil64(one_tiles * p, sms) * (ceil64(steps, p) * one_clocks + store) + (p > 1 ? join : 0);
+        if (cost < least) {
+            least = cost;
+            pair = false;
+            tiles = one_tiles;
+            split = p;
+        }
+    }
+    return pair;
+}
+
 // y[t, :] = x[t, :] w_e^T (columns = false: contraction over w's columns) or
 // x[t, :] w_e (columns = true: over w's rows).
 bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t ldx, const void *w, int64_t ldw,
@@ -351,8 +377,8 @@ bakron_status_t bakron_matmul_grouped_dw(const void *dy_dev, int32_t type, int64
     if (s == BAKRON_OK && rows) s = check_operand(x_dev, k, x_row_stride, 2);
     if (s != BAKRON_OK) return s;
     if (!aligned16(dw_dev)) return BAKRON_ERR_ALIGNMENT;
-    const int64_t tiles = experts * ceil64(n, 128) * ceil64(k, 256);
-    if (tiles > kMaxTiles) return BAKRON_ERR_INVALID_ARG;
+    const int64_t one_tiles = experts * ceil64(n, 128) * ceil64(k, 128);
+    if (one_tiles > kMaxTiles) return BAKRON_ERR_INVALID_ARG;
     int sms = 0;
     if (configure_device(sms) != cudaSuccess) return BAKRON_ERR_CUDA;
     Args g{};
@@ -377,7 +403,10 @@ bakron_status_t bakron_matmul_grouped_dw(const void *dy_dev, int32_t type, int64
     if (!map3(&m.a, t, 2, dy_dev, n, rows, dy_row_stride, 1, rows * dy_row_stride, 64, 64) ||
         !map3(&m.b, t, 2, x_dev, k, rows, x_row_stride, 1, rows * x_row_stride, 64, 64))
         return BAKRON_ERR_CUDA;
-    if (launch_outer(kOuter, m, g, tiles, sms, (cudaStream_t)stream) != cudaSuccess)
+    int64_t tiles = 0;
+    const bool pair = outer_pair(rows, experts, experts * ceil64(n, 256) * ceil64(k, 256), one_tiles, 64, 370, 280, sms,
+                                 tiles, g.split);
+    if (launch_outer(pair ? kOuterPair : kOuterOne, m, g, tiles, sms, (cudaStream_t)stream) != cudaSuccess)
         return BAKRON_ERR_CUDA;
     return BAKRON_OK;
 }
@@ -409,8 +438,8 @@ bakron_status_t bakron_gram_grouped(const void *X_dev, int32_t type, int64_t x_r
     }
     if (s != BAKRON_OK) return s;
     if (!aligned16(A_dev)) return BAKRON_ERR_ALIGNMENT;
-    const int64_t mt = ceil64(d, 128), tiles = experts * (mt * (mt + 1) / 2);
-    if (mt > 16384 || tiles > kMaxTiles) return BAKRON_ERR_INVALID_ARG;
+    const int64_t mt = ceil64(d, 128), one_tiles = experts * (mt * (mt + 1) / 2);
+    if (mt > 16384 || one_tiles > kMaxTiles) return BAKRON_ERR_INVALID_ARG;
     GramGroupedLayout L;
     L.compute(type, rows, d);
     int sms = 0;
@@ -445,7 +474,17 @@ bakron_status_t bakron_gram_grouped(const void *X_dev, int32_t type, int64_t x_r
     }
     m.b = m.a;
     m.b2 = m.a;
-    if (launch_outer(type == BAKRON_F32 ? kGramThree : kGramOne, m, g, tiles, sms, st) != cudaSuccess)
+    // pairs' tiles of a lower triangle: 256 rows, 256 (from three parts 128) columns
+    const int64_t mp = ceil64(d, 256), triangle = mp * (mp + 1) / 2;
+    int64_t tiles = 0;
+    Variant v;
+    if (type == BAKRON_F32)
+        v = outer_pair(rows, experts, experts * (2 * triangle - (mt & 1)), one_tiles, 32, 600, 420, sms, tiles, g.split)
+                ? kGramThreePair : kGramThreeOne;
+    else
+        v = outer_pair(rows, experts, experts * triangle, one_tiles, 64, 370, 280, sms, tiles, g.split)
+                ? kGramPair : kGramOne;
+    if (launch_outer(v, m, g, tiles, sms, st) != cudaSuccess)
         return BAKRON_ERR_CUDA;
     return launch_gram_damp(A_dev, d, (int)experts, damping, g.st, st) == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA;
 }

@@ -70,7 +70,7 @@ struct Shape {
     // a warp's staged steps: two chunks of its columns' (kTokensB), or one of them
     static constexpr int kStepFloats = P::kRagged == kTokensB ? 2 * kCols : kCols;
     // tiles whose contraction a cluster may split (few tiles, one per cluster)
-    static constexpr bool kSplit = P::kRagged != kContract && !P::kPair;
+    static constexpr bool kSplit = !P::kPair;
     static constexpr int kRing = 227 * 1024 - kReserve - kTurnSpace;
     static constexpr int kStages = kRing / kStageBytes < 8 ? kRing / kStageBytes : 8;
     static constexpr int kAcc = P::kPlanes > 1 ? 2 : 1;             // accumulators per buffer
@@ -115,9 +115,9 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; 
 
 // Tiles of tile row i that reach on or below the diagonal of a square result.
 template <class P>
-__host__ __device__ __forceinline__ int lower_tiles_of_row(int i)
+__device__ __forceinline__ int lower_tiles_of_row(const Args &g, int i)
 {
-    return (i * Shape<P>::kM + Shape<P>::kM - 1) / P::kBN + 1;
+    return min((i * Shape<P>::kM + Shape<P>::kM - 1) / P::kBN + 1, ceil_div(g.b_total, P::kBN));
 }
 
 template <class P>
@@ -128,7 +128,7 @@ __device__ __forceinline__ int tiles_of_group(const Args &g, int len)
     if (P::kRagged == kTokensA) return ceil_div(len, kM) * ceil_div(g.b_total, P::kBN);
     if (P::kLower) {
         int n = 0;
-        for (int i = 0; i < ceil_div(g.a_total, kM); ++i) n += lower_tiles_of_row<P>(i);
+        for (int i = 0; i < ceil_div(g.a_total, kM); ++i) n += lower_tiles_of_row<P>(g, i);
         return n;
     }
     return ceil_div(g.a_total, kM) * ceil_div(g.b_total, P::kBN);
@@ -181,7 +181,7 @@ __device__ __forceinline__ Tile find_tile(const Args &g, const int *first, const
     } else {
         int r, c;
         if (P::kLower) {
-            for (r = 0; i >= lower_tiles_of_row<P>(r); ++r) i -= lower_tiles_of_row<P>(r);
+            for (r = 0; i >= lower_tiles_of_row<P>(g, r); ++r) i -= lower_tiles_of_row<P>(g, r);
             c = i;
         } else {
             const int nt = ceil_div(g.b_total, P::kBN);
@@ -767,9 +767,10 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             uint32_t tail_parity = 0;
             for (int t = tile0; t < total; t = next_tile(t)) {
                 const Tile x = find_tile<P>(g, first, order, t);
-                it += ceil_div(x.k1 - x.k0, S::kKB);
+                const int nkb = ceil_div(x.k1 - x.k0, S::kKB);
+                it += stage_end(nkb) - stage_begin(nkb);
                 const int valid = (x.k1 - x.k0) % S::kKB;
-                if (!(valid & 15)) continue;
+                if (!(valid & 15) || (S::kSplit && part != split - 1)) continue;  // (the last part has the last stage)
                 const int s = (it - 1) % S::kStages;
                 if (!__all_sync(0xffffffffu, wait(tail_full_bar(s), (tail_parity >> s) & 1))) break;
                 tail_parity ^= 1u << s;

@@ -23,16 +23,17 @@ namespace bakron {
 namespace mm {
 
 namespace {
+template <bool Pair>
 struct Outer {
     static constexpr Ragged kRagged = kContract;
-    static constexpr bool kPair = true, kEight = false, kAColumns = true, kLower = false;
-    static constexpr int kBN = 256, kPlanes = 1, kKRows = 64, kBoxRows = 64;
+    static constexpr bool kPair = Pair, kEight = false, kAColumns = true, kLower = false;
+    static constexpr int kBN = Pair ? 256 : 128, kPlanes = 1, kKRows = 64, kBoxRows = 64;
 };
-template <int Planes>
+template <int Planes, bool Pair>
 struct Gram {
     static constexpr Ragged kRagged = kContract;
-    static constexpr bool kPair = true, kEight = false, kAColumns = true, kLower = true;
-    static constexpr int kBN = Planes > 1 ? 128 : 256, kPlanes = Planes, kKRows = Planes > 1 ? 32 : 64, kBoxRows = kKRows;
+    static constexpr bool kPair = Pair, kEight = false, kAColumns = true, kLower = true;
+    static constexpr int kBN = Planes > 1 || !Pair ? 128 : 256, kPlanes = Planes, kKRows = Planes > 1 ? 32 : 64, kBoxRows = kKRows;
 };
 
 // Three bf16 parts of an fp32 matrix, each rounded to nearest from what the
@@ -106,18 +107,24 @@ __global__ void gram_damp_kernel(float *__restrict__ A, int64_t d, float damping
 
 cudaError_t configure_outer()
 {
-    cudaError_t e = configure<Outer>();
-    if (e == cudaSuccess) e = configure<Gram<1>>();
-    return e == cudaSuccess ? configure<Gram<3>>() : e;
+    cudaError_t e = configure<Outer<true>>();
+    if (e == cudaSuccess) e = configure<Outer<false>>();
+    if (e == cudaSuccess) e = configure<Gram<1, true>>();
+    if (e == cudaSuccess) e = configure<Gram<1, false>>();
+    if (e == cudaSuccess) e = configure<Gram<3, true>>();
+    return e == cudaSuccess ? configure<Gram<3, false>>() : e;
 }
 
 cudaError_t launch_outer(Variant v, const Maps &maps, const Args &g, int64_t tiles, int sms,
                         cudaStream_t stream)
 {
     switch (v) {
-    case kOuter: return launch<Outer>(maps, g, tiles, sms, stream);
-    case kGramOne: return launch<Gram<1>>(maps, g, tiles, sms, stream);
-    default: return launch<Gram<3>>(maps, g, tiles, sms, stream);
+    case kOuterPair: return launch<Outer<true>>(maps, g, tiles, sms, stream);
+    case kOuterOne: return launch<Outer<false>>(maps, g, tiles, sms, stream);
+    case kGramPair: return launch<Gram<1, true>>(maps, g, tiles, sms, stream);
+    case kGramOne: return launch<Gram<1, false>>(maps, g, tiles, sms, stream);
+    case kGramThreePair: return launch<Gram<3, true>>(maps, g, tiles, sms, stream);
+    default: return launch<Gram<3, false>>(maps, g, tiles, sms, stream);
     }
 }
 
