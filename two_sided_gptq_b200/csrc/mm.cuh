@@ -51,6 +51,9 @@ enum Variant {
 cudaError_t configure_rows();
 cudaError_t configure_eight();
 cudaError_t configure_outer();
+// How many clusters of p CTAs run at once (kernels whose contraction is split hold
+// an SM per CTA, all alike).
+cudaError_t clusters_that_fit(int p, int &n);
 cudaError_t launch_rows(Variant v, const Maps &maps, const Args &g, int64_t tiles, int sms,
                         cudaStream_t stream);
 cudaError_t launch_eight(Variant v, const Maps &maps, const Args &g, int64_t tiles, int sms,

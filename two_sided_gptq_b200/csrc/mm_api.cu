@@ -33,25 +33,34 @@ constexpr int64_t kMaxTiles = (int64_t)1 << 30;
 constexpr int kChunkF32 = 8, kChunk16 = 16;
 
 std::mutex g_mu;
-int g_sms[64] = {};  // SM count of each configured device
+// What a configured device holds at once: SMs, and clusters of p CTAs (one CTA an
+// SM).  Clusters stay within a part of the chip, so that 15 of 8 and 33 of 4 CTAs
+// run on 148 SMs; one more waits for a whole round.
+struct Device {
+    int sms;
+    int clusters[9];
+};
+Device g_devices[64] = {};
 
-// Kernel attributes once per device; the device's SM count.
-cudaError_t configure_device(int &sms)
+// Kernel attributes once per device; the device's limits.
+cudaError_t configure_device(Device &device)
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lk(g_mu);
-    if (!g_sms[dev]) {
-        int n = 0;
-        if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    if (!g_devices[dev].sms) {
+        Device d = {};
+        if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
         if ((e = configure_rows()) != cudaSuccess) return e;
         if ((e = configure_eight()) != cudaSuccess) return e;
         if ((e = configure_outer()) != cudaSuccess) return e;
-        g_sms[dev] = n;
+        for (int p = 1; p <= 8; p *= 2)
+            if ((e = clusters_that_fit(p, d.clusters[p])) != cudaSuccess) return e;
+        g_devices[dev] = d;
     }
-    sms = g_sms[dev];
+    device = g_devices[dev];
     return cudaSuccess;
 }
 
@@ -122,10 +131,10 @@ int64_t row_tiles(int64_t rows, int64_t experts, int64_t tile)
 // CTAs per tile of a call with short groups: while the tiles would leave half
 // the SMs idle the contraction is split, down to two stages a CTA (eight CTAs
 // are the most a cluster holds on every device).
-int split_of(int64_t tiles, int64_t stages, int sms)
+int split_of(int64_t tiles, int64_t stages, const Device &device)
 {
     int s = 1;
-    while (s < 8 && tiles * s * 2 <= sms && stages >= 4 * s) s *= 2;
+    while (s < 8 && tiles <= device.clusters[2 * s] && stages >= 4 * s) s *= 2;
     return s;
 }
 
@@ -134,8 +143,9 @@ int split_of(int64_t tiles, int64_t stages, int sms)
 // tiles over the SMs, at the clocks measured per 128-long step of the
 // contraction (8192 x 14336 x 4096) and for a join of parts.  Half of a group's
 // last tile is empty on average.
-Variant eight_variant(int64_t rows, int64_t n, int64_t k, int64_t experts, int sms, int &split)
+Variant eight_variant(int64_t rows, int64_t n, int64_t k, int64_t experts, const Device &device, int &split)
 {
+    const int sms = device.sms;
     struct Shape { Variant v; int64_t m, w, ctas; double clocks; };
     const Shape shapes[] = {{kEightPair256, 256, 256, 2, 1000}, {kEightPair128, 256, 128, 2, 600},
                             {kEightOne128, 128, 128, 1, 630}};
@@ -149,7 +159,7 @@ Variant eight_variant(int64_t rows, int64_t n, int64_t k, int64_t experts, int s
         const double mean = row_tiles_mean * ceil64(n, s.w);
         const int64_t most = row_tiles(rows, experts, s.m) * ceil64(n, s.w);
         for (int p = 1; p <= (s.ctas == 1 ? 8 : 1); p *= 2) {
-            if (p > 1 && (most * p > sms || steps < 2 * p)) break;
+            if (p > 1 && (most > device.clusters[p] || steps < 2 * p)) break;
             const double cost = ceil(mean * s.ctas * p / sms) * ceil64(steps, p) * s.clocks + (p > 1 ? join : 0);
             if (cost < least) {
                 least = cost;
@@ -166,8 +176,9 @@ Variant eight_variant(int64_t rows, int64_t n, int64_t k, int64_t experts, int s
 // the least time, as above, at the clocks per `step` rows of the contraction.
 // `tiles` is replaced by the number of the tiles taken.
 bool outer_pair(int64_t rows, int64_t experts, int64_t pair_tiles, int64_t one_tiles, int64_t step, double pair_clocks,
-                double one_clocks, int sms, int64_t &tiles, int &split)
+                double one_clocks, const Device &device, int64_t &tiles, int &split)
 {
+    const int sms = device.sms;
     const double store = 2500, join = 1800;
     const int64_t steps = ceil64(ceil64(rows, experts), step);
     double least = ceil64(2 * pair_tiles, sms) * (steps * pair_clocks + 2 * store);
@@ -175,8 +186,8 @@ bool outer_pair(int64_t rows, int64_t experts, int64_t pair_tiles, int64_t one_t
     tiles = pair_tiles;
     split = 1;
     for (int p = 1; p <= 8; p *= 2) {
-        if (p > 1 && (one_tiles * p > sms || steps < 2 * p)) break;
-        const double cost = ceil64(one_tiles * p, sms) * (ceil64(steps, p) * one_clocks + store) + (p > 1 ? join : 0);
+        if (p > 1 && (one_tiles > device.clusters[p] || steps < 2 * p)) break;
+        const double cost = ceil64(one_tiles * p, sms) * (ceil64(steps, p) * one_clocks + store / p) + (p > 1 ? join : 0);
         if (cost < least) {
             least = cost;
             pair = false;
@@ -213,8 +224,8 @@ bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t 
     const int64_t bn = small ? 64 : 256;
     const int64_t tiles = row_tiles(rows, experts, bn) * ceil64(out, 128);
     if (tiles > kMaxTiles) return BAKRON_ERR_INVALID_ARG;
-    int sms = 0;
-    if (configure_device(sms) != cudaSuccess) return BAKRON_ERR_CUDA;
+    Device device;
+    if (configure_device(device) != cudaSuccess) return BAKRON_ERR_CUDA;
     Args g{};
     if ((s = begin(ws, ws_bytes, kStatusBytes, !rows, (cudaStream_t)stream, g)) != BAKRON_OK) return s;
     if (!rows) return BAKRON_OK;
@@ -227,7 +238,7 @@ bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t 
     g.ldo = ldy;
     g.out_type = y_type;
     g.turn = y_type != BAKRON_F32 && ldy % 8 == 0;
-    if (small) g.split = split_of(tiles, ceil64(in, 64), sms);
+    if (small) g.split = split_of(tiles, ceil64(in, 64), device);
     g.idesc = idesc16(type, columns, false);
     g.chunk = y_type == BAKRON_F32 ? kChunkF32 : kChunk16;
     Maps m;
@@ -237,7 +248,7 @@ bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t 
         !map2(&m.b2, t, 2, x, in, rows, ldx, 64, small ? 64 : 128))
         return BAKRON_ERR_CUDA;
     const Variant v = columns ? (small ? kRowsDx64 : kRowsDx256) : (small ? kRows64 : kRows256);
-    if (launch_rows(v, m, g, tiles, sms, (cudaStream_t)stream) != cudaSuccess) return BAKRON_ERR_CUDA;
+    if (launch_rows(v, m, g, tiles, device.sms, (cudaStream_t)stream) != cudaSuccess) return BAKRON_ERR_CUDA;
     return BAKRON_OK;
 }
 
@@ -306,10 +317,10 @@ bakron_status_t bakron_matmul_blocks(const uint8_t *x_dev, int64_t x_row_stride,
     const bool small = rows <= 32 * experts;
     if ((small ? row_tiles(rows, experts, 64) : row_tiles(rows, experts, 128)) * ceil64(n, 128) > kMaxTiles)
         return BAKRON_ERR_INVALID_ARG;
-    int sms = 0;
-    if (configure_device(sms) != cudaSuccess) return BAKRON_ERR_CUDA;
+    Device device;
+    if (configure_device(device) != cudaSuccess) return BAKRON_ERR_CUDA;
     int split = 1;
-    const Variant v = small ? kEightB64 : eight_variant(rows, n, k, experts, sms, split);
+    const Variant v = small ? kEightB64 : eight_variant(rows, n, k, experts, device, split);
     const int64_t m = small ? 64 : v == kEightOne128 ? 128 : 256, bn = v == kEightPair256 ? 256 : 128;
     const int64_t tiles = row_tiles(rows, experts, m) * ceil64(n, bn);
     Args g{};
@@ -328,7 +339,7 @@ bakron_status_t bakron_matmul_blocks(const uint8_t *x_dev, int64_t x_row_stride,
     g.x_steps = x_scales_dev;
     g.w_steps = w_scales_dev;
     g.w_step_rows = w_scale_rows;
-    g.split = small ? split_of(tiles, ceil64(k, 128), sms) : split;
+    g.split = small ? split_of(tiles, ceil64(k, 128), device) : split;
     Maps maps;
     const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     CUtensorMap *xm = small ? &maps.b : &maps.a, *wm = small ? &maps.a : &maps.b;
@@ -337,7 +348,7 @@ bakron_status_t bakron_matmul_blocks(const uint8_t *x_dev, int64_t x_row_stride,
         !map3(wm, t, 1, w_dev, k, n, w_row_stride, experts, w_expert_stride, 128,
               small ? 128 : (uint32_t)(bn * 128 / m)))
         return BAKRON_ERR_CUDA;
-    if (launch_eight(v, maps, g, tiles, sms, (cudaStream_t)stream) !=
+    if (launch_eight(v, maps, g, tiles, device.sms, (cudaStream_t)stream) !=
         cudaSuccess)
         return BAKRON_ERR_CUDA;
     return BAKRON_OK;
@@ -379,8 +390,8 @@ bakron_status_t bakron_matmul_grouped_dw(const void *dy_dev, int32_t type, int64
     if (!aligned16(dw_dev)) return BAKRON_ERR_ALIGNMENT;
     const int64_t one_tiles = experts * ceil64(n, 128) * ceil64(k, 128);
     if (one_tiles > kMaxTiles) return BAKRON_ERR_INVALID_ARG;
-    int sms = 0;
-    if (configure_device(sms) != cudaSuccess) return BAKRON_ERR_CUDA;
+    Device device;
+    if (configure_device(device) != cudaSuccess) return BAKRON_ERR_CUDA;
     Args g{};
     if ((s = begin(ws_dev, ws_bytes, kStatusBytes, !rows, (cudaStream_t)stream, g)) != BAKRON_OK) return s;
     if (!rows) {
@@ -404,9 +415,9 @@ bakron_status_t bakron_matmul_grouped_dw(const void *dy_dev, int32_t type, int64
         !map3(&m.b, t, 2, x_dev, k, rows, x_row_stride, 1, rows * x_row_stride, 64, 64))
         return BAKRON_ERR_CUDA;
     int64_t tiles = 0;
-    const bool pair = outer_pair(rows, experts, experts * ceil64(n, 256) * ceil64(k, 256), one_tiles, 64, 370, 280, sms,
+    const bool pair = outer_pair(rows, experts, experts * ceil64(n, 256) * ceil64(k, 256), one_tiles, 64, 570, 510, device,
                                  tiles, g.split);
-    if (launch_outer(pair ? kOuterPair : kOuterOne, m, g, tiles, sms, (cudaStream_t)stream) != cudaSuccess)
+    if (launch_outer(pair ? kOuterPair : kOuterOne, m, g, tiles, device.sms, (cudaStream_t)stream) != cudaSuccess)
         return BAKRON_ERR_CUDA;
     return BAKRON_OK;
 }
@@ -442,8 +453,8 @@ bakron_status_t bakron_gram_grouped(const void *X_dev, int32_t type, int64_t x_r
     if (mt > 16384 || one_tiles > kMaxTiles) return BAKRON_ERR_INVALID_ARG;
     GramGroupedLayout L;
     L.compute(type, rows, d);
-    int sms = 0;
-    if (configure_device(sms) != cudaSuccess) return BAKRON_ERR_CUDA;
+    Device device;
+    if (configure_device(device) != cudaSuccess) return BAKRON_ERR_CUDA;
     cudaStream_t st = (cudaStream_t)stream;
     Args g{};
     if ((s = begin(ws_dev, ws_bytes, L.total, !rows, st, g)) != BAKRON_OK) return s;
@@ -479,12 +490,12 @@ bakron_status_t bakron_gram_grouped(const void *X_dev, int32_t type, int64_t x_r
     int64_t tiles = 0;
     Variant v;
     if (type == BAKRON_F32)
-        v = outer_pair(rows, experts, experts * (2 * triangle - (mt & 1)), one_tiles, 32, 600, 420, sms, tiles, g.split)
+        v = outer_pair(rows, experts, experts * (2 * triangle - (mt & 1)), one_tiles, 32, 1050, 1250, device, tiles, g.split)
                 ? kGramThreePair : kGramThreeOne;
     else
-        v = outer_pair(rows, experts, experts * triangle, one_tiles, 64, 370, 280, sms, tiles, g.split)
+        v = outer_pair(rows, experts, experts * triangle, one_tiles, 64, 570, 510, device, tiles, g.split)
                 ? kGramPair : kGramOne;
-    if (launch_outer(v, m, g, tiles, sms, st) != cudaSuccess)
+    if (launch_outer(v, m, g, tiles, device.sms, st) != cudaSuccess)
         return BAKRON_ERR_CUDA;
     return launch_gram_damp(A_dev, d, (int)experts, damping, g.st, st) == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA;
 }

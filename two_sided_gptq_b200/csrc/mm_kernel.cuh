@@ -83,7 +83,7 @@ struct Shape {
     // registers: the epilogue's accumulators and two loads in flight need more
     // than a 12-warp CTA's even share (168), the other warps far less
     static constexpr bool kRowSteps = P::kEight && P::kRagged == kTokensA;  // a step per lane and chunk
-    static constexpr bool kSplitRegs = kCols > 64;
+    static constexpr bool kSplitRegs = kCols > 64 || (kSplit && kCols == 64);
     static constexpr int kRegsOthers = 56, kRegsEpilogue = 224;
     // a warpgroup can only take registers that the block was launched with
     static constexpr int kRegsNeeded = 128 * kRegsOthers + 32 * kEpiWarps * kRegsEpilogue;
@@ -788,7 +788,8 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
         if constexpr (S::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsEpilogue));
         const int quad = warp & 3;                   // TMEM lanes [32 quad, 32 quad + 32)
         const int half = (warp - 4) >> 2;            // columns [half kCols, half kCols + kCols)
-        const int lane_row = rank * kBM + quad * 32 + lane, col0 = half * S::kCols;
+        const int lane_row = rank * kBM + quad * 32 + lane;
+        int col0 = half * S::kCols;
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
         float *steps_w = steps_sh + (warp - 4) * S::kStepFloats;
         uint32_t *stage_buf = (uint32_t *)turn_sh + (warp - 4) * kStageWords;  // (not with kTokensB)
@@ -796,7 +797,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
         int chunk = 0;
         bool ok = true;
         for (int t = tile0; t < total && ok; t = next_tile(t)) {
-            const Tile x = find_tile<P>(g, first, order, t);
+            Tile x = find_tile<P>(g, first, order, t);
             const int nkb = ceil_div(x.k1 - x.k0, S::kKB);
             const int kb0 = stage_begin(nkb);
             const int nchunk = ceil_div(stage_end(nkb) - kb0, chunk_stages);
@@ -915,32 +916,42 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             if constexpr (S::kSplit) {
                 if (split > 1) {
                     // This part's MMAs have read all its stages, so its ring can
-                    // take its sums; the first CTA reads the others' there, in
-                    // their order, and the others stay until it has.
+                    // take its sums.  Each part then adds up, in the parts'
+                    // order, its share of the columns, and stores those (one
+                    // CTA adding all of them took 20 us for eight parts of 128
+                    // columns); nobody leaves before everybody has read.
                     float *mine = (float *)smem + (int64_t)col0 * kBM + quad * 32 + lane;
-                    if (part) {
 #pragma unroll
-                        for (int c = 0; c < S::kCols; ++c)
-                            if (c < 16 * loads) mine[c * kBM] = acc[c];
-                    }
+                    for (int c = 0; c < S::kCols; ++c)
+                        if (c < 16 * loads) mine[c * kBM] = acc[c];
                     cluster_sync();
-                    if (!part) {
-                        for (int p = 1; p < split; ++p) {
-                            const uint32_t from = map_rank(smem_u32(mine), p);
+                    const int share = S::kCols / split;  // a power of two, at least four
+                    col0 = half * S::kCols + part * share;
+                    x.nb = min(x.nb, col0 + share);
+                    const uint32_t from = smem_u32(mine + part * share * kBM);
 #pragma unroll
-                            for (int c = 0; c < S::kCols; c += 16)
-                                if (c < 16 * loads) {
-                                    float v[16];  // sixteen loads in flight
+                    for (int c = 0; c < S::kCols; ++c) acc[c] = 0.f;
 #pragma unroll
-                                    for (int i = 0; i < 16; ++i) v[i] = load_cluster(from + (c + i) * (kBM * 4));
+                    for (int c = 0; c < S::kCols / 2; c += 4) {
+                        if (c >= share) break;
+                        float v[8][4];  // up to 32 loads in flight
 #pragma unroll
-                                    for (int i = 0; i < 16; ++i) acc[c + i] += v[i];
-                                }
-                        }
+                        for (int p = 0; p < 8; ++p)
+                            if (p < split) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) v[p][i] = load_cluster(map_rank(from, p) + (c + i) * (kBM * 4));
+                            }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[c + i] = v[0][i];
+#pragma unroll
+                        for (int p = 1; p < 8; ++p)
+                            if (p < split) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) acc[c + i] += v[p][i];
+                            }
                     }
                     cluster_arrive();
                     joined = true;
-                    if (part) break;
                 }
             }
             if (!ok) break;

@@ -115,6 +115,22 @@ cudaError_t configure_outer()
     return e == cudaSuccess ? configure<Gram<3, false>>() : e;
 }
 
+cudaError_t clusters_that_fit(int p, int &n)
+{
+    using S = Shape<Outer<false>>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p);
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = p;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(&n, mm_kernel<Outer<false>>, &cfg);
+}
+
 cudaError_t launch_outer(Variant v, const Maps &maps, const Args &g, int64_t tiles, int sms,
                         cudaStream_t stream)
 {
