@@ -70,7 +70,7 @@ struct Shape {
     // a warp's staged steps: two chunks of its columns' (kTokensB), or one of them
     static constexpr int kStepFloats = P::kRagged == kTokensB ? 2 * kCols : kCols;
     // tiles whose contraction a cluster may split (few tiles, one per cluster)
-    static constexpr bool kSplit = !P::kPair;
+    static constexpr bool kSplit = P::kJoin;
     static constexpr int kRing = 227 * 1024 - kReserve - kTurnSpace;
     static constexpr int kStages = kRing / kStageBytes < 8 ? kRing / kStageBytes : 8;
     static constexpr int kAcc = P::kPlanes > 1 ? 2 : 1;             // accumulators per buffer

@@ -26,13 +26,13 @@ namespace {
 template <bool Pair>
 struct Outer {
     static constexpr Ragged kRagged = kContract;
-    static constexpr bool kPair = Pair, kEight = false, kAColumns = true, kLower = false;
+    static constexpr bool kPair = Pair, kJoin = !Pair, kEight = false, kAColumns = true, kLower = false;
     static constexpr int kBN = Pair ? 256 : 128, kPlanes = 1, kKRows = 64, kBoxRows = 64;
 };
 template <int Planes, bool Pair>
 struct Gram {
     static constexpr Ragged kRagged = kContract;
-    static constexpr bool kPair = Pair, kEight = false, kAColumns = true, kLower = true;
+    static constexpr bool kPair = Pair, kJoin = !Pair, kEight = false, kAColumns = true, kLower = true;
     static constexpr int kBN = Planes > 1 || !Pair ? 128 : 256, kPlanes = Planes, kKRows = Planes > 1 ? 32 : 64, kBoxRows = kKRows;
 };
 

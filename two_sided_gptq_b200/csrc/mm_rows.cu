@@ -21,7 +21,7 @@ namespace {
 template <int BN, bool AColumns>
 struct Rows {
     static constexpr Ragged kRagged = kTokensB;
-    static constexpr bool kPair = BN == 256, kEight = false, kAColumns = AColumns, kLower = false;
+    static constexpr bool kPair = BN == 256, kJoin = !kPair, kEight = false, kAColumns = AColumns, kLower = false;
     static constexpr int kBN = BN, kPlanes = 1, kKRows = 0;
     static constexpr int kBoxRows = BN == 256 ? 64 : 32;
 };
