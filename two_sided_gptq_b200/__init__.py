@@ -426,8 +426,8 @@ def quantize_blocks(x, block_rows=1, *, out=None, ws=None, stream=None, check_st
     steps = lead + (-(-rows // block_rows) if block_rows in (1, 128) else rows, -(-cols // 128))
     if out is None:
         wide = -(-cols // 16) * 16
-        q = torch.empty(lead + (rows, wide), dtype=torch.float8_e4m3fn, device=x.device)
-        q = q[..., :cols] if wide != cols else q
+        strides = (wide, 1) if not lead else (rows * wide, wide, 1)
+        q = torch.empty_strided(x.shape, strides, dtype=torch.float8_e4m3fn, device=x.device)
         scales = torch.empty(steps, dtype=torch.float32, device=x.device)
     else:
         q, scales = out
