@@ -29,8 +29,8 @@
  *     nothing is enqueued.  Errors found on the device (non-SPD pivot,
  *     non-finite input, factor with non-positive diagonal, timed-out wait) are
  *     recorded in a status block in the first 256 bytes of the workspace;
- *     every call clears that block (stream-ordered) before its kernels run, so
- *     bakron_get_status() reports the latest call on that workspace.  A fresh
+ *     every call clears that block (stream-ordered; before its kernels run, or
+ *     by them), so bakron_get_status() reports the latest call on that workspace.  A fresh
  *     workspace needs no initialisation.
  *   - A workspace must not be used by two calls that overlap on the GPU.
  *     Distinct workspaces on distinct streams are independent.

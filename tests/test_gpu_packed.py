@@ -556,6 +556,25 @@ def test_equal_calls_give_equal_bits_and_streams_are_followed(bk):
         assert torch.equal(out, first), name
 
 
+def test_what_a_call_allocates_belongs_to_its_stream(bk, monkeypatch):
+    made, plain = [], bk.workspace
+    monkeypatch.setattr(bk, "workspace", lambda *a: made.append(torch.cuda.current_stream()) or plain(*a))
+    O, side = bounds([0, 30, 30, 97]), torch.cuda.Stream()
+    problems = calls(bk, rows=1000, n=2056, k=2064)
+    for name, (f, shape, dtype) in problems.items():
+        made.clear()
+        side.wait_stream(torch.cuda.current_stream())
+        y = f(O, stream=side, check_status=False)
+        assert made == [side], name
+        side.synchronize()
+        at = y.untyped_storage().data_ptr()
+        del y
+        assert torch.empty(shape, dtype=dtype, device="cuda").data_ptr() != at, name
+    made.clear()
+    bk.quantize_blocks(torch.ones((100, 100), device="cuda"), stream=side)
+    assert made == [side]
+
+
 def test_captured_calls_replay_with_other_offsets(bk):
     a, b = [0, 30, 30, 97], [2, 2, 60, 99]
     for name, (f, shape, dtype) in calls(bk).items():

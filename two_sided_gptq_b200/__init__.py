@@ -14,6 +14,7 @@ Method: "BaKron: Efficient Quantization with Kronecker-Factored Hessians"
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import _native
 from ._native import BakronError, BatchItem, Config, PlanStats, Profile, ProfileLaunch, Quantizer, Status, check
@@ -348,6 +349,19 @@ def _device():
     return _raw_module._cuda_getDevice()
 
 
+def _on_stream(call):
+    """``stream``, if given, is the current one during the call: what the call
+    allocates then belongs to that stream, and the next user of a freed
+    workspace's memory comes after the call's kernels."""
+    @functools.wraps(call)
+    def run(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        with _torch().cuda.stream(stream):
+            return call(*args, **kw)
+    return run
+
+
 def _here(t, name, dims, dtypes, dev):
     """A CUDA tensor on device ``dev`` with unit stride along its last dimension."""
     try:
@@ -407,6 +421,7 @@ def _call(name, args, ws, stream, check_status, dev, need=STATUS_BYTES):
         check(lib.bakron_get_status(at, size, st), name + " (device)")
 
 
+@_on_stream
 def quantize_blocks(x, block_rows=1, *, out=None, ws=None, stream=None, check_status=True):
     """8-bit floating point codes of ``x`` (rows x cols, or batch x rows x cols;
     float32, bfloat16 or float16) with one float32 step per block of
@@ -445,6 +460,7 @@ def quantize_blocks(x, block_rows=1, *, out=None, ws=None, stream=None, check_st
     return q, scales
 
 
+@_on_stream
 def matmul_blocks(x, x_scales, w, w_scales, offsets=None, *, out_dtype=None, out=None, ws=None, stream=None,
                   check_status=True):
     """``y = (x * steps) (w * steps)^T`` of 8-bit (float8_e4m3fn) operands
@@ -515,6 +531,7 @@ def _grouped(name, x, w, offsets, across, out_dtype, out, ws, stream, check_stat
     return y
 
 
+@_on_stream
 def matmul_grouped(x, w, offsets, *, out_dtype=None, out=None, ws=None, stream=None, check_status=True):
     """``y[t] = x[t] w[e]^T`` for the packed rows ``t`` of every expert e
     (``bakron_matmul_grouped``): ``x`` rows x k, ``w`` experts x n x k, both
@@ -524,12 +541,14 @@ def matmul_grouped(x, w, offsets, *, out_dtype=None, out=None, ws=None, stream=N
     return _grouped("bakron_matmul_grouped", x, w, offsets, 2, out_dtype, out, ws, stream, check_status)
 
 
+@_on_stream
 def matmul_grouped_dx(dy, w, offsets, *, out_dtype=None, out=None, ws=None, stream=None, check_status=True):
     """Gradient of :func:`matmul_grouped` for its rows: ``dx[t] = dy[t] w[e]``
     (``bakron_matmul_grouped_dx``)."""
     return _grouped("bakron_matmul_grouped_dx", dy, w, offsets, 1, out_dtype, out, ws, stream, check_status)
 
 
+@_on_stream
 def matmul_grouped_dw(dy, x, offsets, *, out_dtype=None, out=None, ws=None, stream=None, check_status=True):
     """Gradient of :func:`matmul_grouped` for its weights: ``dw[e] = sum_t
     dy[t]^T x[t]`` over expert e's rows, experts x n x k, zeros for an expert
@@ -554,6 +573,7 @@ def matmul_grouped_dw(dy, x, offsets, *, out_dtype=None, out=None, ws=None, stre
     return dw
 
 
+@_on_stream
 def gram_grouped(X, offsets, damping=0.0, *, ws=None, out=None, stream=None, check_status=True):
     """:func:`gram` for every expert of a layer: ``A[e] = X_e^T X_e / N_e +
     damping * mean(diag) * I`` from packed samples ``X`` (rows x d, float32,
