@@ -171,10 +171,16 @@ Variant eight_variant(int64_t rows, int64_t n, int64_t k, int64_t experts, const
     return best;
 }
 
-// Products over the packed rows of a group: CTA pairs' tiles (256 x `width`), or
-// one CTA's (128 x 128), of which up to eight CTAs may share one; whichever needs
-// the least time, as above, at the clocks per `step` rows of the contraction.
-// `tiles` is replaced by the number of the tiles taken.
+// Products over the packed rows of a group: tiles of CTA pairs (256 x 256, from
+// three parts 256 x 128), or of one CTA (128 x 128), whose contraction up to eight
+// may share; whichever needs the least time, as above, at the clocks measured per
+// `step` rows of the contraction (pair 570, one 510 per 64 rows of 16 bits; 1050
+// and 1250 per 32 rows of three parts), for a tile's stores and for a join.
+// Measured, pairs and one CTA a tile: dw 2048 x 2048, 2 experts, 8192 rows 59 and
+// 88 us; 76 x 3788, 23 experts, 1191 rows 43 and 25 us; Gram factors at d = 1024
+// of 4 experts from 4096 fp32 rows 56 and 39 us, d = 1612 of one expert from 5844
+// rows 114 and 133 us; shared by eight: dw 256 x 256 from 16384 rows 82 and 17 us.
+// `tiles` and `split` are set for the tile taken.
 bool outer_pair(int64_t rows, int64_t experts, int64_t pair_tiles, int64_t one_tiles, int64_t step, double pair_clocks,
                 double one_clocks, const Device &device, int64_t &tiles, int &split)
 {

@@ -26,7 +26,8 @@
 // Warp roles: warp 0 lane 0 issues TMA into a ring of kStages stages; warp 1
 // owns TMEM and issues the MMAs; warps 4..11 read finished accumulator chunks
 // (a few stages each, double buffered in TMEM) and add them in FP32 registers,
-// scaled by the 8-bit operands' steps where there are any.  The tensor cores'
+// scaled by the 8-bit operands' steps where there are any.  With kJoin the CTAs of
+// a cluster may share one tile's contraction (Args::split).  The tensor cores'
 // accumulator truncates, so an FP32 result's sums are kept short there.  Where the
 // packed rows are the contraction, warp 3 zeroes what a group's last stage
 // holds beyond the group.

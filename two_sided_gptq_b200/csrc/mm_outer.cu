@@ -9,14 +9,17 @@
 // what three TF32 products would and keep 24 bits instead of 21.
 //
 // Tiles are 256 x 256 (256 x 128 from three parts, whose two accumulators fill
-// tensor memory) by CTA pairs; only those that reach the lower triangle are
+// tensor memory) by CTA pairs, or 128 x 128 by one CTA, whose contraction up to
+// eight CTAs may share, where there are few of the former; only those that reach the lower triangle are
 // formed, the rest is their mirror image.  A tile costs its group's length, so
 // groups are taken longest first in rounds that run forth and back.
 // Measured: dw of 16384 rows, 8 experts, 4096 x 1024 into fp32 121 us (1.14
 // PFLOP/s; 104 us without its stores); Gram factors of 4 experts at d = 4096
 // from 16384 bf16 rows 266 us (220 without the stores: 268 MB, both halves of
 // every matrix); 8 experts at d = 1024 from 8192 fp32 rows 73 us: 12 to split
-// the samples, 51 for the products, 5 for the damping.
+// the samples, 51 for the products (by either tile), 5 for the damping.  By pairs
+// and as it is chosen: dw 512 x 512 from 4096 rows 28.4 and 12.9 us; Gram factors
+// of 2 experts at d = 384 from 30000 rows 80 and 22 us.
 #include "mm_kernel.cuh"
 
 namespace bakron {
