@@ -350,7 +350,7 @@ def _device():
 
 
 def _on_stream(call):
-    """``stream``, if given, is the current one during the call: what the call
+    """Takes the call's ``stream``, which is the current one during it: what the call
     allocates then belongs to that stream, and the next user of a freed
     workspace's memory comes after the call's kernels."""
     @functools.wraps(call)
@@ -406,14 +406,14 @@ def _result(out, shape, dtype, allowed, dev):
     return out
 
 
-def _call(name, args, ws, stream, check_status, dev, need=STATUS_BYTES):
+def _call(name, args, ws, check_status, dev, need=STATUS_BYTES):
     """One library call on a workspace: ``ws``, or a new one."""
     if ws is None:
         ws = workspace(need, dev)
     elif ws.get_device() != dev or ws.dtype != _bytes or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous uint8 tensor on the current device")
     lib, at, size = _native._lib or _lib(), ws.data_ptr(), ws.numel()
-    st = _raw_module._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    st = _raw_module._cuda_getCurrentRawStream(dev)
     status = getattr(lib, name)(*args, at, size, st)
     if status:
         check(status, name)
@@ -456,7 +456,7 @@ def quantize_blocks(x, block_rows=1, *, out=None, ws=None, stream=None, check_st
     ldx = _ld(x, -2, cols, 1)
     _call("bakron_quantize_blocks",
           (x.data_ptr(), _type_ids[x.dtype], batch, rows, cols, x.stride(0) if batch > 1 else 0, ldx, block_rows,
-           q.data_ptr(), ldq, scales.data_ptr()), ws, stream, check_status, dev)
+           q.data_ptr(), ldq, scales.data_ptr()), ws, check_status, dev)
     return q, scales
 
 
@@ -505,12 +505,12 @@ def matmul_blocks(x, x_scales, w, w_scales, offsets=None, *, out_dtype=None, out
     _call("bakron_matmul_blocks",
           (x.data_ptr(), x.stride(0) if rows > 1 else wide, x_scales.data_ptr(), w.data_ptr(), ldw,
            stride[0] if experts > 1 else (n * ldw + 15) // 16 * 16, w_scales.data_ptr(), 1 if per_row else 128, at,
-           experts, y.data_ptr(), types[y.dtype], y.stride(0) if rows > 1 else n, rows, n, k), ws, stream, check_status,
+           experts, y.data_ptr(), types[y.dtype], y.stride(0) if rows > 1 else n, rows, n, k), ws, check_status,
           dev)
     return y
 
 
-def _grouped(name, x, w, offsets, across, out_dtype, out, ws, stream, check_status):
+def _grouped(name, x, w, offsets, across, out_dtype, out, ws, check_status):
     dev = _device()
     _here(x, "x" if across == 2 else "dy", (2,), _half, dev)
     dtype = x.dtype
@@ -527,7 +527,7 @@ def _grouped(name, x, w, offsets, across, out_dtype, out, ws, stream, check_stat
     ldw = _ld(w, 1, k, 8)
     _call(name, (x.data_ptr(), _type_ids[dtype], _ld(x, 0, into, 8), w.data_ptr(), ldw,
                  w.stride(0) if experts > 1 else n * ldw, offsets.data_ptr(), experts, y.data_ptr(),
-                 _type_ids[y.dtype], _ld(y, 0, width, 1), rows, n, k), ws, stream, check_status, dev)
+                 _type_ids[y.dtype], _ld(y, 0, width, 1), rows, n, k), ws, check_status, dev)
     return y
 
 
@@ -538,14 +538,14 @@ def matmul_grouped(x, w, offsets, *, out_dtype=None, out=None, ws=None, stream=N
     bfloat16 or float16, ``offsets`` int32 with experts + 1 row bounds on the
     device.  Sums in float32; ``y`` rows x n of x's type or float32.  Rows
     outside every group keep what ``out`` holds (unspecified in a new result)."""
-    return _grouped("bakron_matmul_grouped", x, w, offsets, 2, out_dtype, out, ws, stream, check_status)
+    return _grouped("bakron_matmul_grouped", x, w, offsets, 2, out_dtype, out, ws, check_status)
 
 
 @_on_stream
 def matmul_grouped_dx(dy, w, offsets, *, out_dtype=None, out=None, ws=None, stream=None, check_status=True):
     """Gradient of :func:`matmul_grouped` for its rows: ``dx[t] = dy[t] w[e]``
     (``bakron_matmul_grouped_dx``)."""
-    return _grouped("bakron_matmul_grouped_dx", dy, w, offsets, 1, out_dtype, out, ws, stream, check_status)
+    return _grouped("bakron_matmul_grouped_dx", dy, w, offsets, 1, out_dtype, out, ws, check_status)
 
 
 @_on_stream
@@ -569,7 +569,7 @@ def matmul_grouped_dw(dy, x, offsets, *, out_dtype=None, out=None, ws=None, stre
         raise ValueError("out must be contiguous")
     _call("bakron_matmul_grouped_dw",
           (dy.data_ptr(), _type_ids[x.dtype], _ld(dy, 0, n, 8), x.data_ptr(), _ld(x, 0, k, 8), offsets.data_ptr(),
-           experts, dw.data_ptr(), _type_ids[dw.dtype], rows, n, k), ws, stream, check_status, dev)
+           experts, dw.data_ptr(), _type_ids[dw.dtype], rows, n, k), ws, check_status, dev)
     return dw
 
 
@@ -591,7 +591,7 @@ def gram_grouped(X, offsets, damping=0.0, *, ws=None, out=None, stream=None, che
     t = _type_ids[X.dtype]
     need = _lib().bakron_gram_grouped_workspace_size(t, rows, d) if ws is None else 0
     _call("bakron_gram_grouped", (X.data_ptr(), t, _ld(X, 0, d, 8), offsets.data_ptr(), experts, float(damping),
-                                  A.data_ptr(), rows, d), ws, stream, check_status, dev, need)
+                                  A.data_ptr(), rows, d), ws, check_status, dev, need)
     return A
 
 
