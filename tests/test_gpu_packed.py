@@ -129,6 +129,28 @@ def test_quantize_nothing_and_nonfinite(bk):
     bk.quantize_blocks(rand((150, 300), 1).cuda())  # the next call starts clean
 
 
+@pytest.mark.parametrize("block_rows,few,many", [(1, (1984, 130), (1985, 130)), (1, (992, 1025), (993, 1025)),
+                                                 (128, (260, 8000), (260, 10700)), (1, (1, 1), (70, 30000))])
+def test_quantize_reports_from_any_block(bk, block_rows, few, many):
+    """Grids of one, a few hundred and more blocks of threads on one workspace."""
+    ws = bk.workspace(256).fill_(255)  # a fresh workspace holds anything
+    for shape in (few, many, few):
+        x = rand(shape, 1).cuda()
+        q, s = bk.quantize_blocks(x, block_rows, ws=ws)
+        want_q, want_s = packed.quantize(x.cpu(), block_rows)
+        assert torch.equal(s.double().cpu(), want_s)
+        assert torch.equal(q.float().double().cpu(), want_q)
+        for at in {(0, 0), (shape[0] - 1, shape[1] - 1), (shape[0] // 2, shape[1] // 3)}:
+            y = x.clone()
+            y[at] = float("nan")
+            with pytest.raises(bk.BakronError) as e:
+                bk.quantize_blocks(y, block_rows, ws=ws)
+            assert e.value.status == bk.Status.ERR_NONFINITE
+            assert bk.get_status(ws) == bk.Status.OK
+            bk.quantize_blocks(y, block_rows, ws=ws, check_status=False)
+            bk.quantize_blocks(x, block_rows, ws=ws)  # the next call starts clean
+
+
 # ------------------------------------------------------------ 8-bit products
 def eight(rows, k, seed):
     """Codes over the whole range, steps over several powers of two."""
