@@ -578,6 +578,29 @@ def test_equal_calls_give_equal_bits_and_streams_are_followed(bk):
         assert torch.equal(out, first), name
 
 
+def test_calls_on_two_streams_at_once(bk):
+    """Split and whole contractions of two streams share the device."""
+    a, b = calls(bk, rows=3000, n=200, k=264), calls(bk, rows=700, n=1104, k=1032)
+    for p, x in ((a, rand((3000, 264), 4).cuda()), (b, rand((700, 1032), 5).cuda())):
+        p["gram fp32"] = (lambda o, x=x, **kw: bk.gram_grouped(x, o, **kw), p["gram fp32"][1], F32)
+    oa, ob = bounds([0, 1000, 1010, 3000]), bounds([0, 30, 400, 700])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for name in a:
+        sides = [(p[name][0], o, p[name][1], p[name][2]) for p, o in ((a, oa), (b, ob))]
+        want = [f(o) for f, o, _, _ in sides]
+        outs = [[torch.zeros(shape, dtype=t, device="cuda") for _ in range(8)] for _, _, shape, t in sides]
+        spaces = [bk.workspace(2 ** 25) for _ in sides]
+        torch.cuda.synchronize()
+        for i in range(8):
+            for (f, o, _, _), out, ws, stream in zip(sides, outs, spaces, streams):
+                f(o, out=out[i], ws=ws, stream=stream, check_status=False)
+        for ws, stream in zip(spaces, streams):
+            assert bk.get_status(ws, stream) == bk.Status.OK
+        torch.cuda.synchronize()
+        for out, w in zip(outs, want):
+            assert all(torch.equal(y, w) for y in out), name
+
+
 def test_what_a_call_allocates_belongs_to_its_stream(bk, monkeypatch):
     made, plain = [], bk.workspace
     monkeypatch.setattr(bk, "workspace", lambda *a: made.append(torch.cuda.current_stream()) or plain(*a))

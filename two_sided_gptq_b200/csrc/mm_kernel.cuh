@@ -470,6 +470,10 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     auto acce_bar = [&](int b) { return bar0 + 8u * (4 * S::kStages + S::kBufs + b); };
     const uint32_t drain_bar = bar0 + 8u * (4 * S::kStages + 2 * S::kBufs);
     static_assert(4 * S::kStages + 2 * S::kBufs + 1 <= 48, "barriers");
+    static_assert(48 * 8 + (kMaxExperts + 4) * 4 + 1024 +
+                          (P::kEight ? S::kEpiWarps * S::kStepFloats * 4 : kMaxExperts * 2) <= kReserve,
+                  "what lies behind the ring");
+    static_assert(!S::kSplit || S::kStages * S::kStageBytes >= kBM * BN * 4, "a part's sums take its ring");
     // accumulator chunk number c: its buffer and the parity of its buffer's use
     auto buf_of = [](int c) { return c % S::kBufs; };
     auto use_of = [](int c) { return c / S::kBufs & 1; };
