@@ -377,8 +377,9 @@ bakron_status_t bakron_proxy_loss(const float *W_dev, const float *V_dev, const 
  * decrease and must lie in [0, rows]; a group may be empty.  Rows outside every
  * group are neither read into a result nor written.  The host never reads the
  * offsets, so a call can be captured into a CUDA graph and replayed with other
- * ones.  A group whose bounds are not a valid range counts as empty, and
- * BAKRON_ERR_INVALID_ARG is recorded (device error).
+ * ones.  A group whose bounds are not a valid range, or that begins before the
+ * end of an earlier range, counts as empty, and BAKRON_ERR_INVALID_ARG is
+ * recorded (device error).
  *
  * experts is 1 .. 1024, extents are at most 2^30.  Matrices are row-major with
  * unit column stride; *_row_stride is in elements.  Operands that the tensor

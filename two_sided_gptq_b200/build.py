@@ -34,7 +34,9 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "bakron.h"), __file__]
+    deps = sources() + [os.path.join(ROOT, "include", "bakron.h"), __file__]
+    for pattern in ("*.cuh", "*.h"):
+        deps += glob.glob(os.path.join(CSRC, pattern))
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -10,6 +10,7 @@
 #include "common.cuh"
 #include "kernels.cuh"
 #include "mm.cuh"
+#include "mm_groups.h"
 
 using namespace bakron;
 
@@ -119,13 +120,6 @@ bool map3(CUtensorMap *m, CUtensorMapDataType t, int64_t size, const void *p, in
     const uint64_t strides[2] = {(uint64_t)(stride * size), (uint64_t)(plane_stride * size)};
     const uint32_t box[3] = {box_cols, box_rows, 1};
     return encode_tensor_map(m, t, 3, p, dims, strides, box);
-}
-
-// Tiles a call can have at most: every group adds at most one partial tile of
-// packed rows, and a group without rows adds none.
-int64_t row_tiles(int64_t rows, int64_t experts, int64_t tile)
-{
-    return rows / tile + (experts < rows ? experts : rows);
 }
 
 // CTAs per tile of a call with short groups: while the tiles would leave half

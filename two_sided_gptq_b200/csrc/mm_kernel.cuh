@@ -41,6 +41,7 @@
 
 #include "common.cuh"
 #include "mm.cuh"
+#include "mm_groups.h"
 #include "tcgen05.cuh"
 
 namespace bakron {
@@ -50,6 +51,7 @@ using namespace tc;
 
 constexpr int kBM = 128;
 constexpr int kMaxSorted = 128;  // groups up to which they are sorted by length
+constexpr uint16_t kNoRows = 0x8000;  // beside a group's number: it counts as empty, whatever its bounds
 constexpr int kReserve = 10 * 1024;  // barriers, tile numbering, alignment, staged steps
 
 template <class P>
@@ -97,7 +99,7 @@ struct Tile {
     int e, a0, na, b0, nb, k0, k1, count;
 };
 
-// Group e's packed rows [lo, hi), empty if the offsets are not a valid range.
+// Group e's packed rows [lo, hi), empty if its bounds are no range.
 __device__ __forceinline__ bool group_range(const Args &g, int e, int &lo, int &hi)
 {
     if (!g.offsets) {
@@ -107,7 +109,7 @@ __device__ __forceinline__ bool group_range(const Args &g, int e, int &lo, int &
     }
     lo = __ldg(g.offsets + e);
     hi = __ldg(g.offsets + e + 1);
-    if (lo >= 0 && lo <= hi && hi <= g.rows) return true;
+    if (is_range(lo, hi, g.rows)) return true;
     lo = hi = 0;
     return false;
 }
@@ -156,9 +158,10 @@ __device__ __forceinline__ Tile find_tile(const Args &g, const int *first, const
         else b = m;
     }
     Tile x;
-    x.e = P::kRagged == kContract ? order[a] : a;
+    x.e = P::kRagged == kContract ? order[a] & ~kNoRows : a;
     int lo, hi;
     group_range(g, x.e, lo, hi);
+    if (P::kRagged == kContract && (order[a] & kNoRows)) lo = hi = 0;
     int i = t - first[a];
     x.count = hi - lo;
     if (P::kRagged == kTokensB) {
@@ -511,32 +514,40 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     }
     pdl_wait();  // everything below may touch what earlier kernels wrote
     if (warp == 2) {
-        // tile numbering: exclusive prefix sum of the groups' tile counts;
-        // where a tile's cost is its group's length, longest groups first
-        int base = 0;
+        // tile numbering: exclusive prefix sum of the groups' tile counts, those
+        // of groups whose rows no earlier group has; where a tile's cost is its
+        // group's length, longest groups first
+        int base = 0, reach = 0;
         const int fixed = P::kRagged == kContract ? tiles_of_group<P>(g, 0) : 0;
-        if (P::kRagged == kContract) {
-            for (int e = lane; e < g.experts; e += 32) {
-                int lo, hi, place = e;
-                group_range(g, e, lo, hi);
-                if (g.experts <= kMaxSorted) {
-                    place = 0;
-                    for (int o = 0; o < g.experts; ++o) {
-                        int a, b;
-                        group_range(g, o, a, b);
-                        place += b - a > hi - lo || (b - a == hi - lo && o < e);
-                    }
-                }
-                order[place] = (uint16_t)e;
-            }
-        }
         for (int e0 = 0; e0 < g.experts; e0 += 32) {
             const int e = e0 + lane;
+            int lo = 0, hi = 0;
+            const bool range = e < g.experts && group_range(g, e, lo, hi);
+            int most = hi;  // the largest end up to this group
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, most, o);
+                if (lane >= o) most = max(most, v);
+            }
+            const int before = __shfl_up_sync(0xffffffffu, most, 1);
+            const bool rows = range && has_rows(lo, hi, g.rows, lane ? max(reach, before) : reach);
+            reach = max(reach, __shfl_sync(0xffffffffu, most, 31));
             int n = 0;
             if (e < g.experts) {
-                int lo, hi;
-                if (!group_range(g, e, lo, hi)) error_sh = BAKRON_ERR_INVALID_ARG;
-                n = P::kRagged == kContract ? fixed : tiles_of_group<P>(g, hi - lo);
+                if (!rows) error_sh = BAKRON_ERR_INVALID_ARG;
+                n = P::kRagged == kContract ? fixed : rows ? tiles_of_group<P>(g, hi - lo) : 0;
+                if (P::kRagged == kContract) {
+                    int place = e;
+                    if (g.experts <= kMaxSorted) {
+                        place = 0;
+                        for (int o = 0; o < g.experts; ++o) {
+                            int a, b;
+                            group_range(g, o, a, b);
+                            place += b - a > hi - lo || (b - a == hi - lo && o < e);
+                        }
+                    }
+                    order[place] = (uint16_t)e | (rows ? 0 : kNoRows);
+                }
             }
             int inc = n;
 #pragma unroll
@@ -554,9 +565,16 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     if (kPair) cluster_sync();  // the other CTA's barriers exist before anything signals them
     tc_fence_after();
     const uint32_t tmem_base = tmem_base_sh;
-    const int total = first[g.experts];
     const int chunk_stages = P::kEight ? 1 : g.chunk;
     const int tile0 = blockIdx.x / (S::kCtas * split), tile_step = gridDim.x / (S::kCtas * split);
+    // The host launches a cluster per tile where a contraction is split.  A second
+    // tile would need the join's barriers again, which have no time limit, so none
+    // is taken even if the bounds change while the kernels of a call read them.
+    int total = first[g.experts];
+    if (S::kSplit && split > 1 && total > tile_step) {
+        total = tile_step;
+        if (threadIdx.x == 0) error_sh = BAKRON_ERR_INVALID_ARG;
+    }
     // The tile after t.  Where a tile's cost is its group's length, every other
     // round runs backwards, so that who had a long tile gets a short one.
     auto next_tile = [&](int t) {
