@@ -489,6 +489,21 @@ size_t bakron_selftest_band_abort_workspace_size(void);
 bakron_status_t bakron_selftest_band_abort(int32_t timeout_ms, void *ws_dev, size_t ws_bytes,
                                            bakron_stream_t stream);
 
+/* Failure-detection self-test of the packed-row products' way out: one product
+ * of zeros (the 16-bit kernel by CTA pairs, two tiles for one pair), laid out in
+ * ws_dev, in which one epilogue warp takes its last wait of the first tile as run
+ * out while its neighbours' waits succeed.  Every other wait then ends with it or
+ * after timeout_ms (1..10000); the kernel records BAKRON_ERR_DEVICE_TIMEOUT in
+ * the status block at the start of ws_dev, leaves the results that the warp's
+ * column half would have stored as they were (0xff bytes, from byte 1024 on),
+ * frees its tensor memory and exits, leaving the context usable.  ws_dev: at
+ * least bakron_selftest_rows_abort_workspace_size() bytes, 16-byte aligned; its
+ * contents are not read.  Asynchronous on `stream`: read the result with
+ * bakron_get_status. */
+size_t bakron_selftest_rows_abort_workspace_size(void);
+bakron_status_t bakron_selftest_rows_abort(int32_t timeout_ms, void *ws_dev, size_t ws_bytes,
+                                           bakron_stream_t stream);
+
 /* Static description of a status code. */
 const char *bakron_status_string(bakron_status_t status);
 

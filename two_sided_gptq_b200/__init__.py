@@ -22,8 +22,8 @@ from ._native import BakronError, BatchItem, Config, PlanStats, Profile, Profile
 __all__ = ["factor", "solve", "solve_host", "proxy_loss", "plan_stats", "last_profile",
            "last_profile_launches", "tune_leaf", "tune_cache_key", "tune_cache_get", "tune_cache_put",
            "solve_batch", "gram", "gram_grouped", "quantize_blocks", "matmul_blocks", "matmul_grouped",
-           "matmul_grouped_dx", "matmul_grouped_dw", "selftest_wait_timeout", "selftest_band_abort", "workspace", "get_status",
-           "BakronError", "Status", "version", "library_path"]
+           "matmul_grouped_dx", "matmul_grouped_dw", "selftest_wait_timeout", "selftest_band_abort",
+           "selftest_rows_abort", "workspace", "get_status", "BakronError", "Status", "version", "library_path"]
 
 
 # bakron_config_t.leaf values bakron_tune_leaf times (one ms_out entry each)
@@ -101,6 +101,20 @@ def selftest_band_abort(timeout_ms: int, ws=None, stream=None):
         ws = workspace(need)
     check(_lib().bakron_selftest_band_abort(int(timeout_ms), _ptr(ws), ws.numel(), _stream(stream)),
           "bakron_selftest_band_abort")
+    return ws
+
+
+def selftest_rows_abort(timeout_ms: int, ws=None, stream=None):
+    """Launch the packed-row products' abort-path self-test
+    (``bakron_selftest_rows_abort``): a product in which one epilogue warp's wait
+    counts as run out and its neighbours' do not.  Returns the workspace; its
+    status then reads ``Status.ERR_DEVICE_TIMEOUT`` (read it with
+    :func:`get_status`)."""
+    need = _lib().bakron_selftest_rows_abort_workspace_size()
+    if ws is None:
+        ws = workspace(need)
+    check(_lib().bakron_selftest_rows_abort(int(timeout_ms), _ptr(ws), ws.numel(), _stream(stream)),
+          "bakron_selftest_rows_abort")
     return ws
 
 

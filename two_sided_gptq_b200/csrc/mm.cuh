@@ -40,6 +40,7 @@ struct Args {
 enum Variant {
     kRows256, kRows64,          // y = x w^T: packed rows on D's columns, tiles of 256 / 64
     kRowsDx256, kRowsDx64,      // dx = dy w
+    kRowsAbort,                 // kRows256 with a wait that counts as run out (self-test)
     kOuterPair, kOuterOne,      // dw = dy^T x, by tiles of a CTA pair / of one CTA
     kGramPair, kGramOne,        // X^T X from 16-bit samples
     kGramThreePair, kGramThreeOne,  // X^T X from three bf16 parts of fp32 samples

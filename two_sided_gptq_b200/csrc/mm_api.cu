@@ -252,6 +252,13 @@ bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t 
     return BAKRON_OK;
 }
 
+// The self-test's problem: two tiles of 256 x 256 for one CTA pair, each of two
+// accumulator chunks, behind the status block.
+struct AbortLayout {
+    static constexpr int64_t rows = 256, n = 512, k = 2 * 64 * kChunk16;
+    static constexpr size_t y = kAlign, x = y + rows * n * 2, w = x + rows * k * 2, total = w + n * k * 2;
+};
+
 struct GramGroupedLayout {
     int64_t ld;
     size_t status, planes, total;
@@ -498,6 +505,42 @@ bakron_status_t bakron_gram_grouped(const void *X_dev, int32_t type, int64_t x_r
     if (launch_outer(v, m, g, tiles, device.sms, st) != cudaSuccess)
         return BAKRON_ERR_CUDA;
     return launch_gram_damp(A_dev, d, (int)experts, damping, g.st, st) == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA;
+}
+
+size_t bakron_selftest_rows_abort_workspace_size(void) { return AbortLayout::total; }
+
+bakron_status_t bakron_selftest_rows_abort(int32_t timeout_ms, void *ws_dev, size_t ws_bytes, bakron_stream_t stream)
+{
+    using L = AbortLayout;
+    if (timeout_ms < 1 || timeout_ms > 10000) return BAKRON_ERR_INVALID_ARG;
+    Args g{};
+    Device device;
+    Maps m;
+    cudaStream_t st = (cudaStream_t)stream;
+    const bakron_status_t s = begin(ws_dev, ws_bytes, L::total, false, st, g);
+    if (s != BAKRON_OK) return s;
+    if (configure_device(device) != cudaSuccess) return BAKRON_ERR_CUDA;
+    char *ws = (char *)ws_dev;
+    if (cudaMemsetAsync(ws + L::y, 0xff, L::x - L::y, st) != cudaSuccess ||
+        cudaMemsetAsync(ws + L::x, 0, L::total - L::x, st) != cudaSuccess)
+        return BAKRON_ERR_CUDA;
+    g.timeout_ns = (uint64_t)timeout_ms * 1000000ull;
+    g.experts = 1;
+    g.rows = (int)L::rows;
+    g.a_total = (int)L::n;
+    g.k_total = (int)L::k;
+    g.out = ws + L::y;
+    g.ldo = L::n;
+    g.out_type = BAKRON_BF16;
+    g.turn = 1;
+    g.idesc = idesc16(BAKRON_BF16, false, false);
+    g.chunk = kChunk16;
+    const CUtensorMapDataType t = map_type(BAKRON_BF16);
+    if (!map3(&m.a, t, 2, ws + L::w, L::k, L::n, L::k, 1, L::n * L::k, 64, 128) ||
+        !map2(&m.b, t, 2, ws + L::x, L::k, L::rows, L::k, 64, 64) ||
+        !map2(&m.b2, t, 2, ws + L::x, L::k, L::rows, L::k, 64, 128))
+        return BAKRON_ERR_CUDA;
+    return launch_rows(kRowsAbort, m, g, 1, device.sms, st) == cudaSuccess ? BAKRON_OK : BAKRON_ERR_CUDA;
 }
 
 }  // extern "C"

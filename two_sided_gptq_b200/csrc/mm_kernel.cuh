@@ -54,6 +54,11 @@ constexpr int kMaxSorted = 128;  // groups up to which they are sorted by length
 constexpr uint16_t kNoRows = 0x8000;  // beside a group's number: it counts as empty, whatever its bounds
 constexpr int kReserve = 10 * 1024;  // barriers, tile numbering, alignment, staged steps
 
+// Self-test of the way out (bakron_selftest_rows_abort): one epilogue warp's last
+// wait of its first tile counts as run out, its neighbours' do not.
+template <class P>
+constexpr bool kGivesUp = false;
+
 template <class P>
 struct Shape {
     static constexpr int kCtas = P::kPair ? 2 : 1;
@@ -317,8 +322,27 @@ __device__ __forceinline__ void store_tile(const Args &g, const Tile &x, int lan
 // a column half turn 32 packed rows at a time in shared memory and write whole
 // 256-byte row pieces.  (Written from the accumulators' own lanes, a warp's
 // store is 64 bytes: 128 of them per thread held the next tile's MMAs up.)
+// All four warps come here or none: half_agrees() decides for them, and its
+// barrier stands before the first use of the buffer.
 constexpr int kTurnRows = 32;
 constexpr int kTurnBytes = kTurnRows * kBM * 2;
+// Whether `ok` holds in all four warps of a column half, which meet here.  A wait
+// that has run out, or that another role's giving up has ended, may have failed in
+// one of them and not in its neighbours.
+__device__ __forceinline__ bool half_agrees(int half, bool ok)
+{
+    uint32_t all;
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((uint32_t)ok), "r"(1 + half)
+        : "memory");
+    return all != 0;
+}
 template <class P, typename T, int N>
 __device__ __forceinline__ void store_turned(const Args &g, const Tile &x, int rank, int thread, int half,
                                              const float (&acc)[N], T *buf)
@@ -334,7 +358,7 @@ __device__ __forceinline__ void store_turned(const Args &g, const Tile &x, int r
 #pragma unroll
     for (int c0 = 0; c0 < N; c0 += kTurnRows) {
         if (col0 + c0 >= x.nb) break;
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+        if (c0) asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
 #pragma unroll
         for (int c = 0; c < kTurnRows; ++c) {
             const float v = acc[c0 + c];
@@ -976,6 +1000,16 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                     cluster_arrive();
                     joined = true;
                 }
+            }
+            if constexpr (kGivesUp<P>) {
+                if (warp == 4 && rank == 0 && t == tile0) {
+                    error_sh = BAKRON_ERR_DEVICE_TIMEOUT;
+                    atomicExch(&abort_sh, 1);
+                    ok = false;
+                }
+            }
+            if constexpr (S::kTurn) {
+                if (g.turn) ok = half_agrees(half, ok);
             }
             if (!ok) break;
             if (P::kEight && P::kRagged == kTokensA && g.w_step_rows == 1) {

@@ -25,7 +25,11 @@ struct Rows {
     static constexpr int kBN = BN, kPlanes = 1, kKRows = 0;
     static constexpr int kBoxRows = BN == 256 ? 64 : 32;
 };
+struct RowsAbort : Rows<256, false> {};
 }  // namespace
+
+template <>
+constexpr bool kGivesUp<RowsAbort> = true;
 
 cudaError_t configure_rows()
 {
@@ -33,6 +37,7 @@ cudaError_t configure_rows()
     if (e == cudaSuccess) e = configure<Rows<64, false>>();
     if (e == cudaSuccess) e = configure<Rows<256, true>>();
     if (e == cudaSuccess) e = configure<Rows<64, true>>();
+    if (e == cudaSuccess) e = configure<RowsAbort>();
     return e;
 }
 
@@ -43,6 +48,7 @@ cudaError_t launch_rows(Variant v, const Maps &maps, const Args &g, int64_t tile
     case kRows256: return launch<Rows<256, false>>(maps, g, tiles, sms, stream);
     case kRows64: return launch<Rows<64, false>>(maps, g, tiles, sms, stream);
     case kRowsDx256: return launch<Rows<256, true>>(maps, g, tiles, sms, stream);
+    case kRowsAbort: return launch<RowsAbort>(maps, g, tiles, sms, stream);
     default: return launch<Rows<64, true>>(maps, g, tiles, sms, stream);
     }
 }
