@@ -489,19 +489,23 @@ size_t bakron_selftest_band_abort_workspace_size(void);
 bakron_status_t bakron_selftest_band_abort(int32_t timeout_ms, void *ws_dev, size_t ws_bytes,
                                            bakron_stream_t stream);
 
-/* Failure-detection self-test of the packed-row products' way out: one product
- * of zeros (the 16-bit kernel by CTA pairs, two tiles for one pair), laid out in
- * ws_dev, in which one epilogue warp takes its last wait of the first tile as run
- * out while its neighbours' waits succeed.  Every other wait then ends with it or
- * after timeout_ms (1..10000); the kernel records BAKRON_ERR_DEVICE_TIMEOUT in
- * the status block at the start of ws_dev, leaves the results that the warp's
- * column half would have stored as they were (0xff bytes, from byte 1024 on),
- * frees its tensor memory and exits, leaving the context usable.  ws_dev: at
- * least bakron_selftest_rows_abort_workspace_size() bytes, 16-byte aligned; its
- * contents are not read.  Asynchronous on `stream`: read the result with
- * bakron_get_status. */
+/* Failure-detection self-test of the packed-row products' ways out: one product
+ * of zeros by the 16-bit kernel's CTA pairs, laid out in ws_dev.
+ *   way 1  two tiles; one epilogue warp takes its last wait of the first tile as
+ *          run out while its neighbours' waits succeed.
+ *   way 2  one tile; the epilogue of one CTA gives up before the last chunk of
+ *          the contraction once all matrix instructions are issued.  The second
+ *          word of the status block then says 1 if they had finished when tensor
+ *          memory was released, 2 if not.
+ * Every other wait ends with that or after timeout_ms (1..10000); the kernel
+ * records BAKRON_ERR_DEVICE_TIMEOUT in the status block at the start of ws_dev,
+ * leaves the results that those warps would have stored as they were (0xff bytes,
+ * from byte 1024 on), frees its tensor memory and exits, leaving the context
+ * usable.  ws_dev: at least bakron_selftest_rows_abort_workspace_size() bytes,
+ * 16-byte aligned; its contents are not read.  Asynchronous on `stream`: read the
+ * result with bakron_get_status. */
 size_t bakron_selftest_rows_abort_workspace_size(void);
-bakron_status_t bakron_selftest_rows_abort(int32_t timeout_ms, void *ws_dev, size_t ws_bytes,
+bakron_status_t bakron_selftest_rows_abort(int32_t timeout_ms, int32_t way, void *ws_dev, size_t ws_bytes,
                                            bakron_stream_t stream);
 
 /* Static description of a status code. */

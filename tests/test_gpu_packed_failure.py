@@ -54,3 +54,17 @@ def test_one_warp_gives_up(bk, timeout_ms):
         assert ((y == -1) | (y == 0)).all()               # the others what they had
         assert (y[:, 128:256] == 0).all()                 # (the other CTA's first tile was complete)
         check_product(bk, ws)
+
+
+def test_epilogue_gives_up_while_the_last_products_run(bk):
+    """Tensor memory is released only once every issued matrix instruction has
+    finished, also where nobody is left to read its result."""
+    ws = None
+    for _ in range(5):
+        ws = bk.selftest_rows_abort(20, ws, way=2)
+        torch.cuda.synchronize()
+        assert ws[4:8].view(torch.int32).item() == 1
+        assert bk.get_status(ws) == bk.Status.ERR_DEVICE_TIMEOUT
+        y = ws[1024: 1024 + 256 * 512 * 2].view(torch.int16).view(256, 512)
+        assert (y[:, :128] == -1).all() and (y[:, 128:256] == 0).all() and (y[:, 256:] == -1).all()
+        check_product(bk, ws)

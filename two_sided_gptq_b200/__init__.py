@@ -104,16 +104,17 @@ def selftest_band_abort(timeout_ms: int, ws=None, stream=None):
     return ws
 
 
-def selftest_rows_abort(timeout_ms: int, ws=None, stream=None):
+def selftest_rows_abort(timeout_ms: int, ws=None, *, way=1, stream=None):
     """Launch the packed-row products' abort-path self-test
     (``bakron_selftest_rows_abort``): a product in which one epilogue warp's wait
-    counts as run out and its neighbours' do not.  Returns the workspace; its
-    status then reads ``Status.ERR_DEVICE_TIMEOUT`` (read it with
+    counts as run out and its neighbours' do not (``way`` 1), or in which the
+    epilogue gives up while the last matrix instructions run (2).  Returns the
+    workspace; its status then reads ``Status.ERR_DEVICE_TIMEOUT`` (read it with
     :func:`get_status`)."""
     need = _lib().bakron_selftest_rows_abort_workspace_size()
     if ws is None:
         ws = workspace(need)
-    check(_lib().bakron_selftest_rows_abort(int(timeout_ms), _ptr(ws), ws.numel(), _stream(stream)),
+    check(_lib().bakron_selftest_rows_abort(int(timeout_ms), int(way), _ptr(ws), ws.numel(), _stream(stream)),
           "bakron_selftest_rows_abort")
     return ws
 

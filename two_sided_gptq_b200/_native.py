@@ -88,7 +88,7 @@ SIGNATURES = {
     "bakron_selftest_band_abort_workspace_size": (_sz, []),
     "bakron_selftest_band_abort": (ctypes.c_int, [ctypes.c_int32, _vp, _sz, _vp]),
     "bakron_selftest_rows_abort_workspace_size": (_sz, []),
-    "bakron_selftest_rows_abort": (ctypes.c_int, [ctypes.c_int32, _vp, _sz, _vp]),
+    "bakron_selftest_rows_abort": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, _vp, _sz, _vp]),
     "bakron_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "bakron_plan_stats": (ctypes.c_int, [_i64, _i64, ctypes.POINTER(Config), ctypes.POINTER(PlanStats)]),
     "bakron_version": (ctypes.c_char_p, []),

@@ -34,6 +34,7 @@ struct Args {
     int split;                       // CTAs that share a tile's contraction (kernels that can split)
     DeviceStatus *st;
     uint64_t timeout_ns;
+    int gives_up;                    // self-test only
 };
 
 // A product of the library: which kernel variant runs it.

@@ -252,8 +252,8 @@ bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t 
     return BAKRON_OK;
 }
 
-// The self-test's problem: two tiles of 256 x 256 for one CTA pair, each of two
-// accumulator chunks, behind the status block.
+// The self-test's problem: one or two tiles of 256 x 256 for one CTA pair, each of
+// two accumulator chunks, behind the status block.
 struct AbortLayout {
     static constexpr int64_t rows = 256, n = 512, k = 2 * 64 * kChunk16;
     static constexpr size_t y = kAlign, x = y + rows * n * 2, w = x + rows * k * 2, total = w + n * k * 2;
@@ -509,10 +509,11 @@ bakron_status_t bakron_gram_grouped(const void *X_dev, int32_t type, int64_t x_r
 
 size_t bakron_selftest_rows_abort_workspace_size(void) { return AbortLayout::total; }
 
-bakron_status_t bakron_selftest_rows_abort(int32_t timeout_ms, void *ws_dev, size_t ws_bytes, bakron_stream_t stream)
+bakron_status_t bakron_selftest_rows_abort(int32_t timeout_ms, int32_t way, void *ws_dev, size_t ws_bytes,
+                                           bakron_stream_t stream)
 {
     using L = AbortLayout;
-    if (timeout_ms < 1 || timeout_ms > 10000) return BAKRON_ERR_INVALID_ARG;
+    if (timeout_ms < 1 || timeout_ms > 10000 || way < 1 || way > 2) return BAKRON_ERR_INVALID_ARG;
     Args g{};
     Device device;
     Maps m;
@@ -527,7 +528,7 @@ bakron_status_t bakron_selftest_rows_abort(int32_t timeout_ms, void *ws_dev, siz
     g.timeout_ns = (uint64_t)timeout_ms * 1000000ull;
     g.experts = 1;
     g.rows = (int)L::rows;
-    g.a_total = (int)L::n;
+    g.a_total = (int)(way == 1 ? L::n : L::n / 2);
     g.k_total = (int)L::k;
     g.out = ws + L::y;
     g.ldo = L::n;
@@ -535,6 +536,7 @@ bakron_status_t bakron_selftest_rows_abort(int32_t timeout_ms, void *ws_dev, siz
     g.turn = 1;
     g.idesc = idesc16(BAKRON_BF16, false, false);
     g.chunk = kChunk16;
+    g.gives_up = way;
     const CUtensorMapDataType t = map_type(BAKRON_BF16);
     if (!map3(&m.a, t, 2, ws + L::w, L::k, L::n, L::k, 1, L::n * L::k, 64, 128) ||
         !map2(&m.b, t, 2, ws + L::x, L::k, L::rows, L::k, 64, 64) ||

@@ -54,8 +54,11 @@ constexpr int kMaxSorted = 128;  // groups up to which they are sorted by length
 constexpr uint16_t kNoRows = 0x8000;  // beside a group's number: it counts as empty, whatever its bounds
 constexpr int kReserve = 10 * 1024;  // barriers, tile numbering, alignment, staged steps
 
-// Self-test of the way out (bakron_selftest_rows_abort): one epilogue warp's last
-// wait of its first tile counts as run out, its neighbours' do not.
+// Self-test of the ways out (bakron_selftest_rows_abort), by Args::gives_up: 1, one
+// epilogue warp's last wait of its first tile counts as run out, its neighbours' do
+// not; 2, the epilogue gives up before the last chunk once all MMAs are issued, and
+// the status block's `where` says 1 if they had finished when tensor memory was
+// released.
 template <class P>
 constexpr bool kGivesUp = false;
 
@@ -480,6 +483,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     float *steps_sh = (float *)(first + kMaxExperts + 4);     // staged row steps (8-bit)
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh, error_sh;
+    [[maybe_unused]] __shared__ volatile int issued_sh;  // (self-test)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = kPair ? (int)cluster_rank() : 0;
@@ -521,6 +525,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
         mbar_init(drain_bar, 1);
         abort_sh = 0;
         error_sh = 0;
+        if constexpr (kGivesUp<P>) issued_sh = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -801,11 +806,16 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                     }
                 }
             }
-            if (!ok) {
-                // let issued MMAs finish before TMEM is released
-                commit(drain_bar);
+            if constexpr (kGivesUp<P>) issued_sh = ok;
+            // Issued MMAs finish before tensor memory is released, also where the
+            // epilogue gives up while the last of them run: the last chunk's commit
+            // says so, or one more where the loop was left inside a chunk.
+            const uint32_t done_bar = ok ? accf_bar(buf_of(chunk - 1)) : drain_bar;
+            const uint32_t done_parity = ok ? use_of(chunk - 1) : 0;
+            if (!ok) commit(drain_bar);
+            if (!ok || chunk) {
                 const uint64_t t0 = now_ns();
-                while (!mbar_try_wait(drain_bar, 0) && now_ns() - t0 < g.timeout_ns + 50000000ull) {
+                while (!mbar_try_wait(done_bar, done_parity) && now_ns() - t0 < g.timeout_ns + 50000000ull) {
                 }
             }
         } else if (warp == 3 && P::kRagged == kContract) {
@@ -956,6 +966,17 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                                 col0 + j < x.nb ? __ldg(g.x_steps + (int64_t)(x.b0 + col0 + j) * nkb + kb0 + c) * s : 0.f;
                         __syncwarp();
                     }
+                    if constexpr (kGivesUp<P>) {
+                        if (g.gives_up == 2 && rank == 0 && c == nchunk - 1) {
+                            const uint64_t t0 = now_ns();
+                            while (!issued_sh && now_ns() - t0 < g.timeout_ns) {
+                            }
+                            error_sh = BAKRON_ERR_DEVICE_TIMEOUT;
+                            atomicExch(&abort_sh, 1);
+                            ok = false;
+                            break;
+                        }
+                    }
                     take(0.f, steps);
                     ok = __all_sync(0xffffffffu, ok);
                 }
@@ -1002,7 +1023,7 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                 }
             }
             if constexpr (kGivesUp<P>) {
-                if (warp == 4 && rank == 0 && t == tile0) {
+                if (g.gives_up == 1 && warp == 4 && rank == 0 && t == tile0) {
                     error_sh = BAKRON_ERR_DEVICE_TIMEOUT;
                     atomicExch(&abort_sh, 1);
                     ok = false;
@@ -1056,6 +1077,9 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     __syncthreads();
     if (threadIdx.x == 0) report(g.st, error_sh);
     if (kPair) cluster_sync();  // neither CTA leaves while the other can still reach its memory
+    if constexpr (kGivesUp<P>) {  // (its two chunks: each buffer's first use)
+        if (g.gives_up == 2 && rank == 0 && threadIdx.x == 0) g.st->where = mbar_try_wait(accf_bar(1), 0) ? 1 : 2;
+    }
     if (warp == 1) {
         tc_fence_after();
         if (kPair)
