@@ -617,16 +617,16 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
     volatile int *abort_flag = &abort_sh;
     bool joined = false;
 
-    // Bounded wait: false once it has run for the time limit or another role
-    // has given up.
-    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    // Bounded wait: false once it has run for the time limit of a pipeline step,
+    // or of `steps` of them, or another role has given up.
+    auto wait = [&](uint32_t bar, uint32_t parity, int steps = 1) -> bool {
         if (mbar_try_wait(bar, parity)) return true;
-        const uint64_t t0 = now_ns();
+        const uint64_t t0 = now_ns(), limit = g.timeout_ns * (uint64_t)min(steps, 1 << 24);  // (600 s at most a step)
         for (;;) {
             for (int i = 0; i < 16; ++i)
                 if (mbar_try_wait(bar, parity)) return true;
             if (*abort_flag) return false;
-            if (now_ns() - t0 > g.timeout_ns) {
+            if (now_ns() - t0 > limit) {
                 error_sh = BAKRON_ERR_DEVICE_TIMEOUT;
                 atomicExch(&abort_sh, 1);
                 return false;
@@ -820,7 +820,8 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
             }
         } else if (warp == 3 && P::kRagged == kContract) {
             // ---------------- zero the tails of this CTA's operands
-            int it = 0;
+            // (a tail may be many stages away: its wait has the limit of them all)
+            int it = 0, last = 0;
             uint32_t tail_parity = 0;
             for (int t = tile0; t < total; t = next_tile(t)) {
                 const Tile x = find_tile<P>(g, first, order, t);
@@ -829,7 +830,8 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
                 const int valid = (x.k1 - x.k0) % S::kKB;
                 if (!(valid & 15) || (S::kSplit && part != split - 1)) continue;  // (the last part has the last stage)
                 const int s = (it - 1) % S::kStages;
-                if (!__all_sync(0xffffffffu, wait(tail_full_bar(s), (tail_parity >> s) & 1))) break;
+                if (!__all_sync(0xffffffffu, wait(tail_full_bar(s), (tail_parity >> s) & 1, it - last + 1))) break;
+                last = it;
                 tail_parity ^= 1u << s;
                 zero_tail<P>(smem + s * S::kStageBytes, valid, (valid + 15) >> 4, lane);
                 if (lane == 0) {
