@@ -980,9 +980,12 @@ bakron_status_t bakron_get_status(void *ws_dev, size_t ws_bytes, bakron_stream_t
     if (cudaStreamSynchronize(s) != cudaSuccess) return BAKRON_ERR_CUDA;
     DeviceStatus h;
     if (cudaMemcpy(&h, ws_dev, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return BAKRON_ERR_CUDA;
-    for (int i = 0; i < kStatusSlots && h.code == 0; ++i) h.code = h.slots[i];
-    if (h.code != 0 && cudaMemset(ws_dev, 0, sizeof(h)) != cudaSuccess) return BAKRON_ERR_CUDA;
-    return (bakron_status_t)h.code;
+    // a call's kernel that reports by CTA runs before those that use the code
+    int32_t first = 0;
+    for (int i = 0; i < kStatusSlots && first == 0; ++i) first = h.slots[i];
+    if (first == 0) first = h.code;
+    if (first != 0 && cudaMemset(ws_dev, 0, sizeof(h)) != cudaSuccess) return BAKRON_ERR_CUDA;
+    return (bakron_status_t)first;
 }
 
 int64_t bakron_get_profile_launches(bakron_profile_launch_t *out, int64_t cap)
