@@ -42,3 +42,35 @@ def test_the_first_error_is_reported(bk, dtype):
         bk.gram_grouped(x, bounds([0, 50, 100]), 0.01, ws=ws, check_status=False)
         assert bk.get_status(ws) == bk.Status.ERR_NONFINITE
         bk.gram_grouped(x, bounds([10, 50, 100]), 0.01, ws=ws)
+
+
+@pytest.mark.parametrize("name", ["blocks", "y", "dx", "dw", "gram"])
+def test_no_report_of_bad_bounds_is_lost(bk, name):
+    """Many calls of one or few blocks of threads, each with bad bounds, each on a
+    status block of its own: the warp that reads the bounds and the thread that
+    sets the block up do not wait for each other before."""
+    calls = 3000
+    x, dy, w = rand((10, 64), 1, BF16), rand((10, 40), 2, BF16), rand((2, 40, 64), 3, BF16)
+    q, s = bk.quantize_blocks(x)
+    wq, ws = bk.quantize_blocks(w, 128)
+    O = bounds([0, 5, 11])
+    f = {
+        "blocks": lambda **kw: bk.matmul_blocks(q, s, wq, ws, O, **kw),
+        "y": lambda **kw: bk.matmul_grouped(x, w, O, **kw),
+        "dx": lambda **kw: bk.matmul_grouped_dx(dy, w, O, **kw),
+        "dw": lambda **kw: bk.matmul_grouped_dw(dy, x, O, **kw),
+        "gram": lambda **kw: bk.gram_grouped(x, O, **kw),
+    }[name]
+    spaces = torch.full((calls, 1024), 255, dtype=torch.uint8, device="cuda")
+    out = f(ws=spaces[0], check_status=False)
+    for i in range(calls):
+        f(ws=spaces[i], out=out, check_status=False)
+    torch.cuda.synchronize()
+    blocks = spaces[:, :256].cpu()
+    assert (blocks[:, :8] == 0).all()                       # no code, no place
+    reports = blocks[:, 8:]
+    assert ((reports == 0) | (reports == int(bk.Status.ERR_INVALID_ARG))).all()
+    lost = (reports == 0).all(1).sum().item()
+    assert lost == 0, f"{lost} of {calls}"
+    # every CTA of a call reports it
+    assert (reports == reports[0]).all()

@@ -524,7 +524,6 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
         }
         mbar_init(drain_bar, 1);
         abort_sh = 0;
-        error_sh = 0;
         if constexpr (kGivesUp<P>) issued_sh = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -547,6 +546,8 @@ mm_kernel(const __grid_constant__ Maps maps, const Args g)
         // of groups whose rows no earlier group has; where a tile's cost is its
         // group's length, longest groups first
         int base = 0, reach = 0;
+        if (lane == 0) error_sh = BAKRON_OK;
+        __syncwarp();
         const int fixed = P::kRagged == kContract ? tiles_of_group<P>(g, 0) : 0;
         for (int e0 = 0; e0 < g.experts; e0 += 32) {
             const int e = e0 + lane;
