@@ -74,7 +74,7 @@ struct Shape {
     static constexpr int kBBytes = P::kRagged == kContract ? kBRows / 64 * kKB * 128 : kBRows * 128;
     static constexpr int kStageBytes = P::kPlanes * (kABytes + kBBytes);
     // shared memory in which results are turned (store_turned, store_staged)
-    static constexpr bool kTurn = P::kRagged == kTokensB && P::kBN == 256;
+    static constexpr bool kTurn = P::kRagged == kTokensB && P::kBN == 256;  // (16-bit operands only)
     static constexpr int kTurnSpace = kTurn ? 2 * 32 * kBM * 2 : P::kRagged == kTokensB ? 0 : 8 * 32 * 17 * 4;
     static constexpr int kEpiWarps = 8;
     static constexpr int kCols = P::kBN / (kEpiWarps / 4);          // columns per epilogue thread
@@ -86,7 +86,7 @@ struct Shape {
     static constexpr int kStages = kRing / kStageBytes < 8 ? kRing / kStageBytes : 8;
     static constexpr int kAcc = P::kPlanes > 1 ? 2 : 1;             // accumulators per buffer
     // accumulator buffers: two, or as many as tensor memory holds where a chunk
-    // is one stage, so that the round trip MMA - epilogue - MMA (about 1000
+    // is one stage, so that the round trip MMA - epilogue - MMA (about 2000
     // clocks, whatever the tile) is shared by several chunks
     static constexpr int kBufs = P::kEight ? (P::kBN == 256 ? 2 : 4) : 2;
     static constexpr int kTmemCols = kBufs * kAcc * P::kBN;
@@ -352,9 +352,6 @@ __device__ __forceinline__ void store_turned(const Args &g, const Tile &x, int r
 {
     const int row0 = rank * kBM;                 // this CTA's first D row
     const int col0 = half * N;
-    float s = 1.f;
-    if (P::kEight && g.w_step_rows == 1 && row0 + thread < x.na)
-        s = __ldg(g.w_steps + (int64_t)x.e * g.a_total + x.a0 + row0 + thread);
     const int piece = (thread & 15) * 8;         // D rows this thread writes: 8 of the CTA's 128
     const int valid = x.na - row0 - piece;
     T *out = (T *)g.out + (int64_t)(x.b0 + col0) * g.ldo + x.a0 + row0 + piece;
@@ -363,10 +360,7 @@ __device__ __forceinline__ void store_turned(const Args &g, const Tile &x, int r
         if (col0 + c0 >= x.nb) break;
         if (c0) asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
 #pragma unroll
-        for (int c = 0; c < kTurnRows; ++c) {
-            const float v = acc[c0 + c];
-            buf[c * kBM + thread] = round_to<T>(P::kEight ? v * s : v);
-        }
+        for (int c = 0; c < kTurnRows; ++c) buf[c * kBM + thread] = round_to<T>(acc[c0 + c]);
         asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
 #pragma unroll
         for (int r = 0; r < kTurnRows; r += 8) {

@@ -313,27 +313,6 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16])
                    "+r"(r[15])::"memory");
 }
 
-// Packed FP32 pairs: d = a b + d and d = d + a, each half rounded by itself.
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi)
-{
-    uint64_t v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
-    return v;
-}
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) { return pack2(__float_as_uint(lo), __float_as_uint(hi)); }
-__device__ __forceinline__ void fma2(uint64_t &d, uint64_t a, uint64_t b)
-{
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ void add2(uint64_t &d, uint64_t a) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(a)); }
-__device__ __forceinline__ void mul2(uint64_t &d, uint64_t a) { asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(a)); }
-// Element c of packed accumulators.
-template <int N>
-__device__ __forceinline__ float element(const uint64_t (&acc)[N], int c)
-{
-    return __uint_as_float((uint32_t)(c & 1 ? acc[c >> 1] >> 32 : acc[c >> 1]));
-}
-
 // 32 lanes (this warp's quarter) x 32 consecutive 32-bit columns into TMEM.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32])
 {
