@@ -136,7 +136,9 @@ int split_of(int64_t tiles, int64_t stages, const Device &device)
 // share a tile's contraction: whichever needs the least time in whole rounds of
 // tiles over the SMs, at the clocks measured per 128-long step of the
 // contraction (8192 x 14336 x 4096) and for a join of parts.  Half of a group's
-// last tile is empty on average.
+// last tile is empty on average.  A tile's first steps and its stores are not
+// counted: for 4100 rows of 16 experts, 4096 x 2048, the estimate is 47 us and 68
+// to 77 are measured.
 Variant eight_variant(int64_t rows, int64_t n, int64_t k, int64_t experts, const Device &device, int &split)
 {
     const int sms = device.sms;
@@ -219,7 +221,8 @@ bakron_status_t grouped_rows(bool columns, const void *x, int32_t type, int64_t 
     if (rows && !aligned16(y)) return BAKRON_ERR_ALIGNMENT;
     // Tiles of 64 packed rows when the groups are short on average: the same
     // weight tile then takes half the stage bytes, so twice the weights are in
-    // flight.
+    // flight.  Beyond that tiles of CTA pairs, which nothing splits: one matrix of
+    // 4096 x 4096 takes 10.9 us with 48 rows and 20.2 with 49, 30 with 1000.
     const bool small = rows <= 48 * experts;
     const int64_t bn = small ? 64 : 256;
     const int64_t tiles = row_tiles(rows, experts, bn) * ceil64(out, 128);
